@@ -295,6 +295,92 @@ int dory_decode_step_mixed(dory_model* m, dory_cache* c,
                            int kv_mode, float* d_logits, int32_t* d_argmax,
                            void* d_workspace, int64_t ws_bytes, void* stream);
 
+/* Draw one token per row of logits (f32 [B] rows of V, `ld` elements apart)
+ * from given uniforms.  Every option is a device array [B], one value per
+ * row, or NULL:
+ *   d_temperature  T; NULL 1; T <= 0 (or NaN) is greedy
+ *   d_top_k        int32; at most this many tokens; NULL or <= 0 off
+ *   d_min_p        only tokens with p >= min_p * max p; NULL or <= 0 off
+ *   d_top_p        the shortest prefix, by descending logit, that holds this
+ *                  share of what top-k and min-p left; NULL or >= 1 off
+ *   d_uniform      u in [0, 1) (required)
+ * With w_i = exp((z_i - max z) / T) the kept tokens are a prefix of the
+ * order (z descending, index ascending) and never none; the token is the
+ * first kept one in index order whose running sum of w exceeds u times the
+ * kept sum (u outside [0, 1) is clamped; the last kept token for u = 1).
+ * Weights and sums are f64.  A -inf or NaN logit is never drawn; tokens at
+ * +inf share the row equally; a row with nothing to draw gets token -1 and
+ * log-probability -inf.  d_tokens int32 [B]; d_logprobs f32 [B] or NULL: the
+ * log-probability of the token in the distribution it was drawn from.
+ * Needs no workspace and allocates nothing.  Enqueued on `stream`.  Errors:
+ * DORY_ERR_ARG (null pointer, B < 0, V < 1, ld < V), DORY_ERR_CUDA.
+ * B = 0 is an empty call. */
+int dory_sample(const float* d_logits, int64_t ld, int B, int V,
+                const float* d_temperature, const int32_t* d_top_k,
+                const float* d_top_p, const float* d_min_p,
+                const float* d_uniform, int32_t* d_tokens, float* d_logprobs,
+                void* stream);
+
+/* One attention layer's K/V entries in 8 bits: 64-token pages of E4M3 codes
+ * behind a block table, with one scale per block of 32 tokens and KV head.
+ * A scale is a power of two, f32, within 2^-126 .. 2^120, and an entry is
+ * scale * e4m3(code).  All buffers are the caller's, 16-byte aligned;
+ * position p of sequence b lives in page block_table[b][p / 64], row p % 64.
+ * Several sequences may share pages that they only read. */
+typedef struct {
+  void* k;                    /* uint8 [n_pages][n_kv_heads][64][head_dim]   */
+  void* v;                    /* the same                                    */
+  float* k_scale;             /* f32 [n_pages][n_kv_heads][2]                */
+  float* v_scale;
+  const int32_t* block_table; /* [batch][pages_per_seq]                      */
+  int n_pages, pages_per_seq, batch, n_kv_heads;
+  int head_dim;               /* 64, 128 or 160                              */
+} dory_kv8;
+
+/* Append K/V rows (bf16 [batch][T][n_kv_heads][head_dim]; *_strides: host
+ * arrays of the element strides of sequence, token and head, multiples of
+ * 8; the head dim is contiguous; base pointers 16-byte aligned) at positions
+ * d_pos[b] .. d_pos[b] + n_b - 1 of every sequence, n_b = d_n[b] (0 <= n_b
+ * <= T, the first n_b rows of a padded batch), or T where d_n is NULL.
+ *   - A 32-token block's scale becomes the least power of two s >= 2^-126
+ *     with |x| <= 448 s for its new rows, or its old scale if that is larger
+ *     and the block holds older rows; new rows are stored as the nearest
+ *     E4M3 code of x / s (ties to even), older rows are brought to s the
+ *     same way.  NaN stays NaN; infinities do not set the scale and are
+ *     stored as +-448 s.  Rows behind position d_pos[b] + n_b keep their
+ *     bytes (under a scale that may have grown they stand for other values).
+ *   - The pages written must belong to one sequence each.
+ *   - A position outside the block table, n_b outside 0..T or a page index
+ *     outside 0..n_pages-1 writes nothing for that sequence (or block) and
+ *     is reported as DORY_ERR_DEVICE by dory_sync_status of any model.
+ * Enqueued on `stream`.  Errors: DORY_ERR_ARG, DORY_ERR_UNSUPPORTED
+ * (head_dim), DORY_ERR_CUDA.  T = 0 is an empty call. */
+int dory_kv8_append(const dory_kv8* c, const void* d_k, const void* d_v,
+                    const int64_t* k_strides, const int64_t* v_strides, int T,
+                    const int32_t* d_pos, const int32_t* d_n, void* stream);
+
+/* Attention of one query token per sequence over the cache:
+ *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j) v_j
+ * over positions j in [max(0, L - window), L), L = d_len[b] (window 0: from
+ * 0), query head h reading KV head h / (n_q_heads / n_kv_heads).  d_q bf16
+ * [batch][n_q_heads][head_dim] (q_strides: host array, element strides of
+ * sequence and head, multiples of 8); d_out bf16, contiguous.  Softmax and
+ * sums are f32.  L = 0 gives zeros.  Rows at positions >= L may hold
+ * anything.  n_q_heads / n_kv_heads must be 1, 2, 4 or 8.
+ *   - d_ws: dory_kv8_workspace_bytes, 256-byte aligned; its contents between
+ *     calls are meaningless.  Calls that may run at the same time need
+ *     workspaces of their own.
+ *   - A length outside 0..64 * pages_per_seq counts as 0, and a page index
+ *     outside 0..n_pages-1 hides that page's keys; both are reported as
+ *     DORY_ERR_DEVICE by dory_sync_status of any model.
+ * Enqueued on `stream`.  Errors: DORY_ERR_ARG, DORY_ERR_UNSUPPORTED
+ * (head_dim, heads per KV head), DORY_ERR_WORKSPACE, DORY_ERR_CUDA. */
+int dory_kv8_workspace_bytes(const dory_kv8* c, int n_q_heads, int64_t* bytes);
+int dory_kv8_attend(const dory_kv8* c, const void* d_q,
+                    const int64_t* q_strides, int n_q_heads,
+                    const int32_t* d_len, int window, float scale, void* d_out,
+                    void* d_ws, int64_t ws_bytes, void* stream);
+
 /* Copy the final residual state s (input of the LM head, f32) of the last
  * call that used this workspace: [B, T, d] for a logits_all prefill, else
  * [B, d]. */

@@ -6,6 +6,7 @@ PyTorch for device memory and streams.
 """
 from ._lib import load, LIB_PATH, DoryError, KV_MODES
 from .model import DoryModel, KVCache, to_device
+from .ops import KV8Pages, sample
 
 __all__ = ["load", "LIB_PATH", "DoryError", "KV_MODES", "DoryModel", "KVCache",
-           "to_device"]
+           "KV8Pages", "sample", "to_device"]

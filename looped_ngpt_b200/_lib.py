@@ -31,6 +31,13 @@ class DoryTensor(Structure):
     _fields_ = [("name", c_char_p), ("d_ptr", c_void_p), ("bytes", c_int64)]
 
 
+class DoryKv8(Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p),
+                ("v_scale", c_void_p), ("block_table", c_void_p),
+                ("n_pages", c_int), ("pages_per_seq", c_int),
+                ("batch", c_int), ("n_kv_heads", c_int), ("head_dim", c_int)]
+
+
 class DoryKernelStat(Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", c_int64),
                 ("total_ms", c_double), ("bytes", c_double),
@@ -69,6 +76,13 @@ SIGNATURES = {
     "dory_debug_bounded_wait": (c_int, [_P, c_int, _P]),
     "dory_debug_gemv": (c_int, [_P, c_char_p, _P, c_int, _P, c_int,
                                 POINTER(c_int), _P]),
+    "dory_sample": (c_int, [_P, c_int64, c_int, c_int, _P, _P, _P, _P, _P, _P,
+                            _P, _P]),
+    "dory_kv8_append": (c_int, [POINTER(DoryKv8), _P, _P, _I64P, _I64P, c_int,
+                                _P, _P, _P]),
+    "dory_kv8_workspace_bytes": (c_int, [POINTER(DoryKv8), c_int, _I64P]),
+    "dory_kv8_attend": (c_int, [POINTER(DoryKv8), _P, _I64P, c_int, _P, c_int,
+                                ctypes.c_float, _P, _P, c_int64, _P]),
     "dory_copy_state": (c_int, [_P, _P, c_int, c_int, c_int, _P, _P]),
     "dory_spec_workspace_bytes": (c_int, [_P, c_int, c_int, _I64P]),
     "dory_spec_decode_step": (c_int, [_P, _P, _P, c_int, c_int, c_int, c_int,

@@ -21,6 +21,20 @@ using namespace dory;
 static __device__ int g_dory_status;   // or-ed ERRBIT_* from device checks
 
 namespace dory {
+int* device_status_word() {
+  constexpr int kMax = 64;
+  static std::mutex mu;
+  static int* addr[kMax];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMax) return nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!addr[dev]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_dory_status) != cudaSuccess) return nullptr;
+    addr[dev] = (int*)p;
+  }
+  return addr[dev];
+}
 namespace {
 thread_local bool t_host_failure = false;
 }

@@ -342,6 +342,61 @@ void launch_spec_accept(const SpecArgs& a, cudaStream_t st);
 void launch_spec_transpose(const int* src, int* dst, int B, int G1,
                            cudaStream_t st);
 
+// -------------------------------------------------------- token sampling ----
+struct SampleArgs {
+  const float* logits;      // [B] rows of V, ld apart
+  int64_t ld;
+  int B, V;
+  const float* temperature; // [B] or null (1)
+  const int* top_k;         // [B] or null (off)
+  const float* top_p;       // [B] or null (off)
+  const float* min_p;       // [B] or null (off)
+  const float* uniform;     // [B]
+  int* tokens;              // [B]
+  float* logprobs;          // [B] or null
+};
+void launch_sample(const SampleArgs& a, cudaStream_t st);
+
+// ------------------------------------------------------- 8-bit K/V cache ----
+constexpr int kKv8Block = 32;        // tokens per scale
+
+// One layer: E4M3 codes [n_pages][Hkv][kPage][hd], scales (powers of two)
+// [n_pages][Hkv][2], pages reached through block_table [B][pages_per_seq].
+struct Kv8 {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  const int* block_table;
+  int n_pages, pages_per_seq, Hkv, hd;
+};
+
+struct Kv8AppendArgs {
+  Kv8 c;
+  int B, T;
+  const bf16 *k, *v;                        // rows [B][T][Hkv][hd] by strides
+  int64_t ks_b, ks_t, ks_h, vs_b, vs_t, vs_h;
+  const int* pos;                           // [B] tokens held before
+  const int* n;                             // [B] rows to append, or null (T)
+  int* err;
+};
+void launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st);
+
+struct Kv8AttendArgs {
+  Kv8 c;
+  int B, G;                                 // G query heads per KV head
+  const bf16* q;                            // [B][Hkv * G][hd] by strides
+  int64_t qs_b, qs_h;
+  const int* len;                           // [B] keys held (the query's own last)
+  int window;                               // 0 = full attention
+  float scale;
+  bf16* out;                                // [B][Hkv * G][hd]
+  void* ws;
+  int* err;
+};
+void launch_kv8_attend(const Kv8AttendArgs& a, cudaStream_t st);
+size_t kv8_attend_ws(int B, int Hkv, int G, int hd);
+
+// Device status word of the current device (null if it cannot be found).
+int* device_status_word();
 // Device status word the tensor-core GEMM reports timeouts to.
 void set_tc_error_word(int* err);
 

@@ -1,0 +1,243 @@
+"""Operators on caller tensors: token sampling and the 8-bit K/V cache of one
+attention layer.  Names follow the C entry points: ``sample`` ->
+``dory_sample``, ``KV8Pages.append`` -> ``dory_kv8_append``,
+``KV8Pages.attend`` -> ``dory_kv8_attend``.
+
+Tensors live on one CUDA device; work goes to ``stream`` (default: that
+device's current stream).  Arguments that do not fit raise ``ValueError``
+before anything is enqueued.
+"""
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import DoryKv8, check
+
+PAGE = 64                 # tokens per page
+BLOCK = 32                # tokens per scale
+
+_I64x3 = ctypes.c_int64 * 3
+_I64x2 = ctypes.c_int64 * 2
+
+
+def _need(t, name, dtype, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: {dtype} {shape} on {device} is needed, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _dense(t, name, dtype, shape, device):
+    _need(t, name, dtype, shape, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t
+
+
+def _strided(t, name, n):
+    """Element strides of the first n dims; the last dim must be contiguous,
+    rows 16-byte aligned (the strides of dims of length 1 do not matter)."""
+    s = [0 if size == 1 else st for size, st in zip(t.shape[:n], t.stride())]
+    if t.stride(-1) != 1 or t.data_ptr() % 16 or any(x % 8 for x in s):
+        raise ValueError(f"{name}: the last dim must be contiguous and every "
+                         "row 16-byte aligned")
+    return s
+
+
+def _cuda(t, name):
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{name}: a CUDA tensor is needed")
+    return t.device
+
+
+class _On:
+    """The device made current and the stream work goes to; outputs allocated
+    inside belong to that stream."""
+
+    __slots__ = ("stream", "ctx")
+
+    def __init__(self, device, stream):
+        if stream is None:
+            self.stream = torch.cuda.current_stream(device)
+            self.ctx = (None if torch.cuda.current_device() == device.index
+                        else torch.cuda.device(device))
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream: on {stream.device}, the tensors are "
+                                 f"on {device}")
+            self.stream, self.ctx = stream, torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def sample(logits, uniform, temperature=None, top_k=None, top_p=None,
+           min_p=None, tokens=None, logprobs=False, stream=None):
+    """Draw one token per row of logits f32 [B, V] (rows may be strided) from
+    uniforms f32 [B] in [0, 1); see dory_sample for the rule.
+
+    temperature, top_p, min_p f32 [B] and top_k int32 [B] are device tensors,
+    one value per row, or None.  tokens: int32 [B] to write, or None.
+    logprobs: True, or an f32 [B] tensor to write.  Returns (tokens, logprobs
+    or None)."""
+    dev = _cuda(logits, "logits")
+    if logits.dtype != torch.float32 or logits.dim() != 2:
+        raise ValueError("logits: float32 [B, V] is needed, got "
+                         f"{logits.dtype} {tuple(logits.shape)}")
+    B, V = logits.shape
+    ld = logits.stride(0) if B > 1 else V
+    if V < 1 or (V > 1 and logits.stride(1) != 1) or ld < V:
+        raise ValueError("logits: rows must be contiguous and apart")
+    f32, i32, row = torch.float32, torch.int32, (B,)
+    _dense(uniform, "uniform", f32, row, dev)
+    for t, name, dt in ((temperature, "temperature", f32),
+                        (top_k, "top_k", i32), (top_p, "top_p", f32),
+                        (min_p, "min_p", f32), (tokens, "tokens", i32)):
+        if t is not None:
+            _dense(t, name, dt, row, dev)
+    with _On(dev, stream) as st:
+        if tokens is None:
+            tokens = torch.empty(row, dtype=i32, device=dev)
+        if isinstance(logprobs, torch.Tensor):
+            lp = _dense(logprobs, "logprobs", f32, row, dev)
+        else:
+            lp = torch.empty(row, dtype=f32, device=dev) if logprobs else None
+        check("dory_sample", _lib.load().dory_sample(
+            logits.data_ptr(), ld, B, V,
+            None if temperature is None else temperature.data_ptr(),
+            None if top_k is None else top_k.data_ptr(),
+            None if top_p is None else top_p.data_ptr(),
+            None if min_p is None else min_p.data_ptr(),
+            uniform.data_ptr(), tokens.data_ptr(),
+            None if lp is None else lp.data_ptr(), st))
+    return tokens, lp
+
+
+class KV8Pages:
+    """One attention layer's K/V entries in 8 bits (dory_kv8): E4M3 codes in
+    64-token pages behind a block table, one power-of-two scale per 32 tokens
+    and KV head.  The tensors are the caller's and are only referred to:
+
+    k, v             uint8 [n_pages, n_kv_heads, 64, head_dim]
+    k_scale, v_scale float32 [n_pages, n_kv_heads, 2]
+    block_table      int32 [batch, pages_per_seq]
+    """
+
+    def __init__(self, k, v, k_scale, v_scale, block_table):
+        dev = _cuda(k, "k")
+        if k.dim() != 4 or k.shape[2] != PAGE or k.shape[3] not in (64, 128, 160):
+            raise ValueError("k: uint8 [n_pages, n_kv_heads, 64, head_dim] with "
+                             "head_dim 64, 128 or 160 is needed, got "
+                             f"{tuple(k.shape)}")
+        shape = tuple(k.shape)
+        _dense(k, "k", torch.uint8, shape, dev)
+        _dense(v, "v", torch.uint8, shape, dev)
+        _dense(k_scale, "k_scale", torch.float32, (shape[0], shape[1], 2), dev)
+        _dense(v_scale, "v_scale", torch.float32, (shape[0], shape[1], 2), dev)
+        if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+            raise ValueError("block_table: int32 [batch, pages_per_seq] is needed")
+        _dense(block_table, "block_table", torch.int32,
+               tuple(block_table.shape), dev)
+        if 0 in shape or 0 in block_table.shape:
+            raise ValueError("an empty cache")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.block_table, self.device = block_table, dev
+        self.n_kv_heads, self.head_dim = shape[1], shape[3]
+        self.batch, self.pages_per_seq = block_table.shape
+        self.c = DoryKv8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                         v_scale.data_ptr(), block_table.data_ptr(), shape[0],
+                         self.pages_per_seq, self.batch, shape[1], shape[3])
+        self._ref = ctypes.byref(self.c)
+        self._ws = {}
+
+    @classmethod
+    def empty(cls, batch, max_ctx, n_kv_heads, head_dim, device="cuda"):
+        """A cache of its own: every sequence owns ceil(max_ctx / 64) pages."""
+        P = -(-max_ctx // PAGE)
+        n = batch * P
+        dev = torch.device(device)
+        z = dict(dtype=torch.uint8, device=dev)
+        o = dict(dtype=torch.float32, device=dev)
+        return cls(torch.zeros((n, n_kv_heads, PAGE, head_dim), **z),
+                   torch.zeros((n, n_kv_heads, PAGE, head_dim), **z),
+                   torch.ones((n, n_kv_heads, 2), **o),
+                   torch.ones((n, n_kv_heads, 2), **o),
+                   torch.arange(n, dtype=torch.int32, device=dev).view(batch, P))
+
+    def append(self, k, v, pos, n=None, stream=None):
+        """Append the first n[b] (None: all) of the rows k, v bf16 [batch, T,
+        n_kv_heads, head_dim] (any strides with 16-byte aligned rows) behind
+        the pos[b] tokens that sequence b holds; pos, n int32 [batch]."""
+        dev, B = self.device, self.batch
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k: bf16 [batch, T, n_kv_heads, head_dim] is needed")
+        T = k.shape[1]
+        shape = (B, T, self.n_kv_heads, self.head_dim)
+        _need(k, "k", torch.bfloat16, shape, dev)
+        _need(v, "v", torch.bfloat16, shape, dev)
+        if T > self.pages_per_seq * PAGE:
+            raise ValueError(f"{T} rows, a sequence holds "
+                             f"{self.pages_per_seq * PAGE}")
+        _dense(pos, "pos", torch.int32, (B,), dev)
+        if n is not None:
+            _dense(n, "n", torch.int32, (B,), dev)
+        if T == 0:
+            return
+        ks, vs = _I64x3(*_strided(k, "k", 3)), _I64x3(*_strided(v, "v", 3))
+        with _On(dev, stream) as st:
+            check("dory_kv8_append", _lib.load().dory_kv8_append(
+                self._ref, k.data_ptr(), v.data_ptr(), ks, vs, T,
+                pos.data_ptr(), None if n is None else n.data_ptr(), st))
+
+    def workspace(self, n_q_heads):
+        """A workspace for attend with n_q_heads query heads."""
+        nb = ctypes.c_int64()
+        with torch.cuda.device(self.device):
+            check("dory_kv8_workspace_bytes",
+                  _lib.load().dory_kv8_workspace_bytes(self._ref, n_q_heads,
+                                                       ctypes.byref(nb)))
+        return torch.empty(nb.value, dtype=torch.uint8, device=self.device)
+
+    def attend(self, q, lens, window=0, scale=None, out=None, ws=None,
+               stream=None):
+        """Attention of one query per sequence, q bf16 [batch, n_q_heads,
+        head_dim], over the lens[b] (int32 [batch]) cached tokens, the last
+        `window` of them if window > 0; scale defaults to 1 / sqrt(head_dim).
+        Returns bf16 [batch, n_q_heads, head_dim] (`out`, if given).  Without
+        `ws` one workspace per stream is kept by this object."""
+        dev, B, hd = self.device, self.batch, self.head_dim
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q: bf16 [batch, n_q_heads, head_dim] is needed")
+        Hq = q.shape[1]
+        shape = (B, Hq, hd)
+        _need(q, "q", torch.bfloat16, shape, dev)
+        if Hq not in [g * self.n_kv_heads for g in (1, 2, 4, 8)]:
+            raise ValueError(f"{Hq} query heads on {self.n_kv_heads} KV heads: "
+                             "1, 2, 4 or 8 per KV head are needed")
+        _dense(lens, "lens", torch.int32, (B,), dev)
+        if window < 0:
+            raise ValueError("window: 0 (off) or more is needed")
+        qs = _I64x2(*_strided(q, "q", 2))
+        if out is not None:
+            _dense(out, "out", torch.bfloat16, shape, dev)
+        with _On(dev, stream) as st:
+            if out is None:
+                out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            if ws is None:
+                key = (st.value, Hq)
+                ws = self._ws.get(key)
+                if ws is None:
+                    ws = self._ws[key] = self.workspace(Hq)
+            check("dory_kv8_attend", _lib.load().dory_kv8_attend(
+                self._ref, q.data_ptr(), qs, Hq, lens.data_ptr(), window,
+                hd ** -0.5 if scale is None else scale, out.data_ptr(),
+                ws.data_ptr(), ws.numel(), st))
+        return out
