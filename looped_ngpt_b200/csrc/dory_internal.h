@@ -393,7 +393,8 @@ struct Kv8AttendArgs {
   int* err;
 };
 void launch_kv8_attend(const Kv8AttendArgs& a, cudaStream_t st);
-size_t kv8_attend_ws(int B, int Hkv, int G, int hd);
+constexpr int kKv8MaxBatch = 2048;  // the attention's block prefix in shared memory
+size_t kv8_attend_ws(int B, int G, int hd);
 
 // Device status word of the current device (null if it cannot be found).
 int* device_status_word();

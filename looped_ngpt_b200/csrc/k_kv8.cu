@@ -1,4 +1,4 @@
-// The 8-bit K/V cache of one layer: appending rows and one-token attention.
+// The 8-bit K/V cache of one layer: appending rows.
 //
 // Codes are E4M3 in 64-token pages [n_pages][Hkv][64][hd]; every block of 32
 // tokens of a page has one scale per KV head, a power of two s = 2^e, and
@@ -86,89 +86,6 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(Kv8AppendArgs a
   if (threadIdx.x == 0) *scale = s;
 }
 
-// ---------------------------------------------------------------- attend ----
-// One block per (KV head, sequence); warp w takes keys w, w + 8, ... with a
-// running maximum and sum per query head, lanes split head_dim.
-constexpr int kAttWarps = 8;
-
-template <int HD, int G>
-__global__ void __launch_bounds__(32 * kAttWarps) kv8_attend_kernel(Kv8AttendArgs a) {
-  constexpr int D = HD / 32;
-  __shared__ float sm[kAttWarps][G], sl[kAttWarps][G], so[kAttWarps][G][HD];
-  const int b = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  pdl_wait();
-  pdl_trigger();
-  int len = a.len[b];
-  if (len < 0 || len > a.c.pages_per_seq * kPage) {
-    if (h == 0 && threadIdx.x == 0) atomicOr(a.err, ERRBIT_BOUNDS);
-    len = 0;
-  }
-  const int lo = a.window ? max(0, len - a.window) : 0;
-  float q[G][D], m[G], l[G], o[G][D];
-  for (int g = 0; g < G; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
-    for (int d = 0; d < D; ++d) {
-      q[g][d] = __bfloat162float(a.q[b * a.qs_b + (int64_t)(h * G + g) * a.qs_h + lane + 32 * d]);
-      o[g][d] = 0.f;
-    }
-  }
-  for (int p = lo + w; p < len; p += kAttWarps) {
-    const int page = a.c.block_table[(size_t)b * a.c.pages_per_seq + p / kPage];
-    if (page < 0 || page >= a.c.n_pages) {
-      if (lane == 0) atomicOr(a.err, ERRBIT_BOUNDS);
-      continue;
-    }
-    const size_t ph = (size_t)page * a.c.Hkv + h;
-    const int r = p % kPage;
-    const float ks = a.c.k_scale[ph * 2 + r / kKv8Block], vs = a.c.v_scale[ph * 2 + r / kKv8Block];
-    const uint8_t* k = a.c.k + (ph * kPage + r) * HD;
-    const uint8_t* v = a.c.v + (ph * kPage + r) * HD;
-    float kf[D], vf[D];
-    for (int d = 0; d < D; ++d) {
-      kf[d] = kv8_decode(k[lane + 32 * d]) * ks;
-      vf[d] = kv8_decode(v[lane + 32 * d]) * vs;
-    }
-    for (int g = 0; g < G; ++g) {
-      float s = 0.f;
-      for (int d = 0; d < D; ++d) s = fmaf(q[g][d], kf[d], s);
-      s = warp_sum(s) * a.scale;
-      const float mn = fmaxf(m[g], s);
-      const float corr = __expf(m[g] - mn), e = __expf(s - mn);
-      l[g] = l[g] * corr + e;
-      for (int d = 0; d < D; ++d) o[g][d] = o[g][d] * corr + e * vf[d];
-      m[g] = mn;
-    }
-  }
-  for (int g = 0; g < G; ++g) {
-    if (lane == 0) { sm[w][g] = m[g]; sl[w][g] = l[g]; }
-    for (int d = 0; d < D; ++d) so[w][g][lane + 32 * d] = o[g][d];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < G * HD; i += 32 * kAttWarps) {
-    const int g = i / HD;
-    float M = -INFINITY, L = 0.f, O = 0.f;
-    for (int k = 0; k < kAttWarps; ++k) M = fmaxf(M, sm[k][g]);
-    for (int k = 0; k < kAttWarps; ++k) {
-      const float f = sm[k][g] == -INFINITY ? 0.f : __expf(sm[k][g] - M);
-      L = fmaf(f, sl[k][g], L);
-      O = fmaf(f, so[k][g][i - g * HD], O);
-    }
-    a.out[((size_t)b * a.c.Hkv + h) * G * HD + i] = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
-  }
-}
-
-template <int HD>
-void attend_hd(const Kv8AttendArgs& a, cudaStream_t st) {
-  const dim3 grid(a.c.Hkv, a.B), block(32 * kAttWarps);
-  switch (a.G) {
-    case 1: launch_k(kv8_attend_kernel<HD, 1>, grid, block, 0, st, a); break;
-    case 2: launch_k(kv8_attend_kernel<HD, 2>, grid, block, 0, st, a); break;
-    case 4: launch_k(kv8_attend_kernel<HD, 4>, grid, block, 0, st, a); break;
-    default: launch_k(kv8_attend_kernel<HD, 8>, grid, block, 0, st, a); break;
-  }
-}
-
 }  // namespace
 
 void launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st) {
@@ -179,16 +96,6 @@ void launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st) {
     case 64: launch_k(kv8_append_kernel<64>, grid, block, 0, st, a); break;
     case 128: launch_k(kv8_append_kernel<128>, grid, block, 0, st, a); break;
     default: launch_k(kv8_append_kernel<160>, grid, block, 0, st, a); break;
-  }
-}
-
-size_t kv8_attend_ws(int, int, int, int) { return 0; }
-
-void launch_kv8_attend(const Kv8AttendArgs& a, cudaStream_t st) {
-  switch (a.c.hd) {
-    case 64: attend_hd<64>(a, st); break;
-    case 128: attend_hd<128>(a, st); break;
-    default: attend_hd<160>(a, st); break;
   }
 }
 

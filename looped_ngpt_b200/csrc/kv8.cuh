@@ -39,6 +39,14 @@ __device__ __forceinline__ float kv8_decode(uint8_t c) {
   return (float)v;
 }
 
+// Two E4M3 codes (low byte first) to f16, exactly: every E4M3 value is an f16.
+__device__ __forceinline__ uint32_t kv8_f16x2(uint32_t codes) {
+  uint32_t r;
+  const uint16_t c = (uint16_t)codes;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+
 // Eight bf16 values times inv -> eight codes.
 __device__ __forceinline__ uint2 kv8_encode8(const uint4& x, float inv) {
   auto two = [&](uint32_t u) {

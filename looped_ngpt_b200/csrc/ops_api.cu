@@ -24,7 +24,7 @@ int check_kv8(const dory_kv8* c) {
       !aligned(c->v_scale, 16) || !aligned(c->block_table, 4))
     return DORY_ERR_ARG;
   // positions are int32; grids take 65535 blocks in y and z
-  if (c->pages_per_seq > INT_MAX / kPage || c->batch > 65535 || c->n_kv_heads > 65535)
+  if (c->pages_per_seq > INT_MAX / kPage || c->batch > 65535 || c->n_kv_heads > 1024)
     return DORY_ERR_UNSUPPORTED;
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 160)
     return DORY_ERR_UNSUPPORTED;
@@ -88,7 +88,12 @@ int dory_kv8_workspace_bytes(const dory_kv8* c, int n_q_heads, int64_t* bytes) {
   if (!bytes || n_q_heads < 1 || n_q_heads % c->n_kv_heads) return DORY_ERR_ARG;
   const int G = n_q_heads / c->n_kv_heads;
   if (G != 1 && G != 2 && G != 4 && G != 8) return DORY_ERR_UNSUPPORTED;
-  *bytes = (int64_t)kv8_attend_ws(c->batch, c->n_kv_heads, G, c->head_dim);
+  // block counts are int32, and every sequence has an entry in shared memory
+  if (c->batch > kKv8MaxBatch ||
+      (int64_t)c->batch * c->pages_per_seq * 2 * c->n_kv_heads > INT_MAX / 2 ||
+      (int64_t)c->n_pages * 2 * c->n_kv_heads > INT_MAX)
+    return DORY_ERR_UNSUPPORTED;
+  *bytes = (int64_t)kv8_attend_ws(c->batch, G, c->head_dim);
   return DORY_OK;
 }
 
