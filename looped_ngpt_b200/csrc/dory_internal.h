@@ -244,6 +244,10 @@ int pf_tile_keys();
 // box_rows x box_cols with box_cols 64 (128-byte swizzle) or 32 (64-byte).
 bool make_map_2d(CUtensorMap* m, const void* ptr, long rows, long cols,
                  long ld, int box_cols, int box_rows);
+// 2-D TMA map over dense bytes [rows][cols], box box_rows x box_cols with
+// box_cols 128, 64 or 32 and the swizzle of that width.
+bool make_map_bytes(CUtensorMap* m, const void* ptr, long rows, long cols,
+                    int box_cols, int box_rows);
 inline bool make_act_map(CUtensorMap* m, const void* ptr, long rows, long cols,
                          int box_cols, int box_rows) {
   return make_map_2d(m, ptr, rows, cols, cols, box_cols, box_rows);
@@ -392,9 +396,16 @@ struct Kv8AttendArgs {
   void* ws;
   int* err;
 };
-void launch_kv8_attend(const Kv8AttendArgs& a, cudaStream_t st);
+// TMA maps of a cache's codes: the first 64 or 128 bytes of a row of K and
+// of V, then (head_dim 160) the last 32.
+struct Kv8Maps {
+  CUtensorMap k, v, k2, v2;
+};
+bool make_kv8_maps(const Kv8& c, Kv8Maps* m);
+void launch_kv8_attend(const Kv8AttendArgs& a, const Kv8Maps& maps,
+                       cudaStream_t st);
 constexpr int kKv8MaxBatch = 2048;  // the attention's block prefix in shared memory
-size_t kv8_attend_ws(int B, int G, int hd);
+size_t kv8_attend_ws(int G, int hd);
 
 // Device status word of the current device (null if it cannot be found).
 int* device_status_word();

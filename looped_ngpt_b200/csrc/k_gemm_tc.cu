@@ -652,6 +652,22 @@ bool make_map_2d(CUtensorMap* m, const void* ptr, long rows, long cols,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_bytes(CUtensorMap* m, const void* ptr, long rows, long cols,
+                    int box_cols, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn || (box_cols != 32 && box_cols != 64 && box_cols != 128)) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+            : box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_kv_tile_map(CUtensorMap* m, const void* ptr, long rows, int hd) {
   auto fn = encode_fn();
   if (!fn) return false;

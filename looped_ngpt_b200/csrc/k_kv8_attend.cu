@@ -7,28 +7,35 @@
 //
 // Work is counted in blocks of 32 positions (one scale each).  The blocks of
 // all (sequence, KV head) pairs are laid end to end and cut into equal runs,
-// one per thread block, whatever the lengths are (they are known on the
-// device only).  Inside a run each of the 8 warps takes every 8th block
-// through its own ring of shared-memory stages, filled by 1-D bulk copies of
-// 4 rows (16 per block), and keeps its own running max, sum and output; the
-// warps meet only where a pair ends.  A pair cut between thread blocks leaves
-// partials (m, l, O) in the workspace, and a second kernel joins them in
-// order; a pair inside one run is finished in place.
+// one per SM and again one per warp, whatever the lengths are (they are known
+// on the device only).  A warp streams its run through its own ring of
+// shared-memory stages, filled by TMA tile loads, with its own running max,
+// sum and output; pairs inside its run it finishes alone.  Pieces of cut
+// pairs (at most two per warp) are joined once the thread block is done, and
+// pieces of pairs cut between thread blocks (at most two each) by a second
+// kernel.  (Joining them in the last thread block to arrive instead, through
+// a fence and a counter per pair, took 3 to 8 us longer than the dependent
+// launch, at every size.)
 //
 // One block in a warp: S^T = K Q^T on m16n8k16 (keys as A rows, the heads as
 // the 8 columns), online softmax per head (lane 4g + t owns heads 2t, 2t+1),
 // P^T by an in-register transpose, O^T += V^T P^T.  Codes become f16 in
 // registers (exact); q is f16 after an exact shift of its row by a power of
 // two (bf16 has 8 significant bits, f16 11; elements 2^-22 below the row's
-// largest lose bits that f32 sums would lose too).  Weights are f16 as
-// p * 2^14: 11 bits, and none above 2^-38 of the largest is lost.  K's scale
-// joins the score's factor, V's the f32 sum into O, so scales of any range
-// are safe.
+// largest lose bits that f32 sums would lose too).  Weights are f16, 11 bits:
+// p * 2^9 against a reference max that moves only when a score passes it by
+// 2^4 (any common reference gives the same o; so most blocks need no
+// rescaling and no reduction across lanes, just one vote), and none above
+// 2^-33 of the largest is lost.  K's scale joins the score's factor; V's
+// scale, relative to the unit O is held in, joins the exponent of p when
+// within 2^2, else the block's product is added in f32.
 //
-// Key 4 g + i of a block (g < 8, i < 4) sits in row group g: 4 rows of one
-// bulk copy.  Fragment row g reads group g, so its 8 rows come from 8 copies,
-// each placed 16 bytes further (mod 128): 16-byte loads of K and transposing
-// ldmatrix of V then hit 8 different bank groups for every head_dim.
+// Row r = 8 i + perm(g) of a block (i < 4) is fragment row g.  Tiles carry the
+// swizzle of their row width (128, 64 or 32 bytes), and perm lets two
+// neighbouring g fall into different halves of the banks, so that 16-byte
+// loads of K and the transposing ldmatrix of V are free of conflicts.  (One
+// TMA instruction per tile: the same blocks as 16 bulk copies of 4 rows cost
+// 160 issue slots per block, a third of the kernel's instructions.)
 #include <algorithm>
 
 #include "async_copy.cuh"
@@ -40,9 +47,12 @@ namespace dory {
 
 namespace {
 
-constexpr int NW = 8;                         // warps
-constexpr int kThreads = 32 * NW;
-constexpr float kShift = 14.f;                // weights are p * 2^14
+// Polls of a bounded wait: about a second (a try_wait that fails suspends the
+// thread for some microseconds).
+constexpr long kPolls = 1L << 18;
+constexpr float kShift = 9.f;                 // weights are p * 2^9 ...
+constexpr float kSlack = 4.f;                 // ... and at most 2^4 more
+constexpr int kNear = 2, kFar = 60;           // V scale / unit: in p; in f32
 
 // 2^x on the SFU (subnormal results flush to zero).
 __device__ __forceinline__ float ex2(float x) {
@@ -51,55 +61,72 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-template <int HD, int G>
+template <int HD>
 struct Att {
   static constexpr int KS = HD / 16;
-  static constexpr int COPY = 4 * HD;                  // bytes of one bulk copy
-  static constexpr int MAT = 8 * (COPY + 16);          // K (or V) of one block
+  static constexpr int W1 = HD == 64 ? 64 : 128;       // bytes of a row's first tile
+  static constexpr int W2 = HD - W1;                   // and of its second (160: 32)
+  static constexpr int MAT = 32 * HD;                  // K (or V) of one block
   static constexpr int STAGE = 2 * MAT;
-  static constexpr int COMB = NW * G * (HD + 2) * 4;   // warp states of a pair
-  static constexpr int NST = std::min(6, (210 * 1024 - COMB) / (NW * STAGE));
-  static constexpr int PART = G * (HD + 2);            // floats of a partial
+  // Warps per thread block and stages per warp, 98 to 131 KB in flight per SM.
+  // More does not help: at head_dim 160, 12 x 1, 8 x 2, 10 x 2 and 7 x 3 take
+  // 420, 443, 448 and 451 us for 64 sequences of 32768 tokens (2.68 GB).
+  static constexpr int NW = HD == 128 ? 8 : 12;
+  static constexpr int NST = HD == 160 ? 1 : 2;
   static constexpr size_t smem(int B) {
-    return 128 + (size_t)NW * NST * STAGE + COMB + (size_t)(2 * B + 1) * 4;
+    return 1024 + (size_t)NW * NST * STAGE + (size_t)(2 * B + 1) * 4;
   }
-  static_assert(NST >= 2, "two stages");
 };
 
-// Byte offset of row group g of a matrix (copies in the order 0 2 4 6 1 3 5 7).
+// Row of fragment row g within 8 rows.
 template <int HD>
-__device__ __forceinline__ int group_off(int g) {
-  return ((g >> 1) + 4 * (g & 1)) * (4 * HD + 16);
+__device__ __forceinline__ int perm(int g) {
+  return HD == 64 ? g : (g >> 1) + 4 * (g & 1);
+}
+// Byte offset of 16-byte chunk c of row r in a block's tiles.
+template <int HD>
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+  if (HD == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  if (c < 8) return r * 128 + ((c ^ (r & 7)) << 4);
+  return 32 * 128 + r * 32 + (((c - 8) ^ ((r >> 2) & 1)) << 4);
 }
 
-// Workspace: prefix of blocks per sequence [B + 1], then two partial slots
-// per thread block (its first pair, its last pair).
-__host__ __device__ inline size_t prefix_bytes(int B) {
-  return ((size_t)(B + 1) * 4 + 255) & ~(size_t)255;
-}
+// A piece of a pair: O[G][hd] (unnormalised), m[G], l[G].
+template <int HD, int G>
+constexpr int kPart = (G * (HD + 2) + 3) & ~3;
 
-// Blocks of the run of one thread block: at least one per warp.
-__device__ __forceinline__ int run_blocks(int total, int grid) {
-  return max((total + grid - 1) / grid, NW);
+// Workspace: two pieces per thread block (of its first pair, and of its
+// last), then one per warp (of its first).
+
+// Length of sequence b (0 if it is out of range), and the number of blocks
+// its visible positions lie in.
+__device__ __forceinline__ int length_of(const Kv8AttendArgs& a, int b) {
+  const int len = a.len[b];
+  return len < 0 || len > a.c.pages_per_seq * kPage ? 0 : len;
+}
+__device__ __forceinline__ int visible_blocks(const Kv8AttendArgs& a, int b) {
+  const int len = length_of(a, b), lo = a.window ? max(0, len - a.window) : 0;
+  return (len + kKv8Block - 1) / kKv8Block - lo / kKv8Block;
 }
 
 template <int HD, int G>
-__global__ void __launch_bounds__(kThreads, 1) kv8_attend_kernel(const Kv8AttendArgs a) {
-  using L = Att<HD, G>;
-  constexpr int KS = L::KS, NST = L::NST;
+__global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
+    const __grid_constant__ Kv8Maps maps, const Kv8AttendArgs a) {
+  using L = Att<HD>;
+  constexpr int KS = L::KS, NST = L::NST, NW = L::NW, kThreads = 32 * NW;
+  constexpr int PART = kPart<HD, G>;
   extern __shared__ uint8_t smraw[];
-  uint8_t* stages = smraw + ((128 - (su32(smraw) & 127)) & 127);
-  float* comb = reinterpret_cast<float*>(stages + NW * NST * L::STAGE);
-  int* pre = reinterpret_cast<int*>(comb + NW * G * (HD + 2));   // [B + 1]
-  int* lens = pre + a.B + 1;                                     // [B]
+  uint8_t* stages = smraw + ((1024 - (su32(smraw) & 1023)) & 1023);
+  int* pre = reinterpret_cast<int*>(stages + NW * NST * L::STAGE);   // [B + 1]
+  int* lens = pre + a.B + 1;                                         // [B]
   __shared__ __align__(8) uint64_t full_[NW][NST];
-  __shared__ int2 meta_[NW][NST];
-  __shared__ int wsum[NW];
+  __shared__ __align__(16) int4 meta_[NW][NST];     // block, pair, scales of K and V
+  __shared__ int wsum[NW], s_piece[2 * NW];
 
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int B = a.B, H = a.c.Hkv;
   uint64_t* full = full_[w];
-  volatile int2* meta = meta_[w];
+  int4* meta = meta_[w];
   if (lane == 0) {
     for (int i = 0; i < NST; ++i) mbar_init(full + i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -113,14 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attend_kernel(const Kv8Attend
     const int b = b0 + tid;
     int n = 0;
     if (b < B) {
-      int len = a.len[b];
-      if (len < 0 || len > a.c.pages_per_seq * kPage) {
-        if (blockIdx.x == 0) atomicOr(a.err, ERRBIT_BOUNDS);
-        len = 0;
-      }
-      lens[b] = len;
-      const int lo = a.window ? max(0, len - a.window) : 0;
-      n = (len + kKv8Block - 1) / kKv8Block - lo / kKv8Block;
+      lens[b] = length_of(a, b);
+      if (blockIdx.x == 0 && lens[b] != a.len[b]) atomicOr(a.err, ERRBIT_BOUNDS);
+      n = visible_blocks(a, b);
     }
     int inc = n;
 #pragma unroll
@@ -141,12 +163,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attend_kernel(const Kv8Attend
   if (tid == 0) pre[0] = 0;
   __syncthreads();
   const int total = pre[B] * H;
-  const int per = run_blocks(total, gridDim.x);
-  const int x0 = min(total, (int)blockIdx.x * per), x1 = min(total, x0 + per);
-  if (blockIdx.x == 0) {
-    int* out = reinterpret_cast<int*>(a.ws);
-    for (int b = tid; b <= B; b += kThreads) out[b] = pre[b];
-  }
+  const int per = (total + gridDim.x - 1) / gridDim.x;
+  const int X0 = (int)min((int64_t)total, (int64_t)blockIdx.x * per), X1 = min(total, X0 + per);
+  const int perw = (X1 - X0 + NW - 1) / NW;
+  const int x0 = min(X1, X0 + w * perw), x1 = min(X1, x0 + perw);
+  float* ws_block = reinterpret_cast<float*>(a.ws);
+  float* ws_warp = ws_block + (size_t)2 * gridDim.x * PART + (size_t)blockIdx.x * NW * PART;
+  if (lane < 2) s_piece[2 * w + lane] = -1;
   for (int b = blockIdx.x; b < B; b += gridDim.x)      // empty sequences
     if (pre[b + 1] == pre[b])
       for (int i = tid; i < H * G * HD; i += kThreads)
@@ -161,69 +184,121 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attend_kernel(const Kv8Attend
     }
     return lo;
   };
+  // first linear block of a pair, and its number of blocks
+  auto start_of = [&](int pair, int* nb) {
+    const int b = pair / H, h = pair - b * H;
+    *nb = pre[b + 1] - pre[b];
+    return pre[b] * H + h * *nb;
+  };
   auto first_block = [&](int b) {
     return a.window ? max(0, lens[b] - a.window) / kKv8Block : 0;
   };
 
-  // ---- this warp's items: blocks x0 + w + NW m ---------------------------
-  const int items = x0 + w < x1 ? (x1 - x0 - w + NW - 1) / NW : 0;
-  int plan_unit = -1, plan_j = 0;      // lane l: item 32 k + l of the batch
+  // ---- this warp's items: blocks x0 + m ------------------------------------
+  const int items = x1 - x0;
+  int plan_u = -1;                     // lane l: item 32 k + l of the batch
+  int4 plan = make_int4(-1, 0, 0, 0);
   const uint32_t st_base = su32(stages + (size_t)w * NST * L::STAGE);
   uint8_t* st_ptr = stages + (size_t)w * NST * L::STAGE;
   auto issue = [&](int m, int s) {
     if ((m & 31) == 0) {
-      const int x = x0 + w + NW * (m + lane);
-      plan_unit = -1;
+      const int x = x0 + m + lane;
+      plan_u = -1;
+      plan.x = -1;                     // no block: a bad page
       if (x < x1) {
         const int b = seq_of(x), nb = pre[b + 1] - pre[b], r = x - pre[b] * H;
-        const int h = r / nb;
-        plan_j = r - h * nb + first_block(b);
-        const int page = a.c.block_table[(size_t)b * a.c.pages_per_seq + (plan_j >> 1)];
-        if (page >= 0 && page < a.c.n_pages) plan_unit = (page * H + h) * 2 + (plan_j & 1);
-        else atomicOr(a.err, ERRBIT_BOUNDS);
+        const int h = r / nb, j = r - h * nb + first_block(b);
+        const int page = a.c.block_table[(size_t)b * a.c.pages_per_seq + (j >> 1)];
+        plan.y = b * H + h;
+        if (page < 0 || page >= a.c.n_pages) {
+          atomicOr(a.err, ERRBIT_BOUNDS);
+        } else {
+          plan_u = (page * H + h) * 2 + (j & 1);
+          plan.x = j;
+          plan.z = __float_as_int(a.c.k_scale[plan_u]);
+          plan.w = __float_as_int(a.c.v_scale[plan_u]);
+        }
       }
     }
-    const int u = __shfl_sync(0xffffffffu, plan_unit, m & 31);
-    const int j = __shfl_sync(0xffffffffu, plan_j, m & 31);
+    const int u = __shfl_sync(0xffffffffu, plan_u, m & 31);
     if (lane == 0) {
-      meta[s].x = u;
-      meta[s].y = j;
-      mbar_expect_tx(full + s, u >= 0 ? 2 * kKv8Block * HD : 0);
+      mbar_expect_tx(full + s, u >= 0 ? 2 * L::MAT : 0);
+      if (u >= 0) {
+        uint8_t* dst = st_ptr + s * L::STAGE;
+        tma_load_2d(dst, &maps.k, 0, u * kKv8Block, full + s);
+        tma_load_2d(dst + L::MAT, &maps.v, 0, u * kKv8Block, full + s);
+        if (L::W2 > 0) {
+          tma_load_2d(dst + 32 * L::W1, &maps.k2, L::W1, u * kKv8Block, full + s);
+          tma_load_2d(dst + L::MAT + 32 * L::W1, &maps.v2, L::W1, u * kKv8Block, full + s);
+        }
+      }
     }
+    if (lane == (m & 31)) meta[s] = plan;
     __syncwarp();
-    if (u >= 0 && lane < 16) {
-      const int gg = lane & 7;
-      const uint8_t* src = (lane < 8 ? a.c.k : a.c.v) + (size_t)u * (kKv8Block * HD) + gg * L::COPY;
-      bulk_load(st_ptr + s * L::STAGE + (lane < 8 ? 0 : L::MAT) + group_off<HD>(gg), src, L::COPY,
-                full + s);
-    }
   };
   for (int m = 0; m < min(NST, items); ++m) issue(m, m);
+  __syncwarp();
 
   bool ok = true;
   int n = 0, s = 0;                    // items done; their stage
   uint32_t ph = 0;                     // and its parity
-  float ks = 0.f, vs = 0.f;            // scales of item n
-  auto load_scales = [&](int stage) {
-    const int u = meta[stage].x;
-    ks = u >= 0 ? a.c.k_scale[u] : 0.f;
-    vs = u >= 0 ? a.c.v_scale[u] : 0.f;
-  };
-  if (items > 0) load_scales(0);
-
-  // ---- the pairs of this run ----------------------------------------------
-  for (int x = x0; x < x1;) {
-    const int b = seq_of(x), nb = pre[b + 1] - pre[b];
-    const int h = (x - pre[b] * H) / nb;
-    const int xs = pre[b] * H + h * nb, xe = xs + nb;  // the pair's blocks
-    const int xn = min(xe, x1);
-    const int len = lens[b], lo = a.window ? max(0, len - a.window) : 0;
-
-    // Q^T fragments: lane (g, t) holds head g; k-step 4c + i of 64-dim chunk
-    // c pairs dims 64c + 16t + 4i + {0, 1} and {2, 3}, as the K loads do
-    uint32_t qf[KS][2];
-    float hs[2];                       // score factors of heads 2t, 2t + 1
-    {
+  int pair = -1, len = 0, lo = 0;      // the current pair
+  uint32_t qf[KS][2];
+  float hs[2] = {0.f, 0.f};            // score factors of heads 2t, 2t + 1
+  float m2[2], c2[2], l2[2], o[KS][4]; // reference max, kShift - it, sum, output
+  int eu = 0;                          // O is held in units of 2^(eu - 127)
+  for (;; ++n) {
+    const int4 it = n < items ? meta[s] : make_int4(0, -1, 0, 0);
+    if (it.y < 0 || it.y != pair) {
+      if (pair >= 0) {
+        // the pair's state in this warp: finished, or a piece: the run's last
+        // in the warp's stages, which are idle by then, its first in the
+        // workspace
+        int nb;
+        const int xs = start_of(pair, &nb);
+        const bool whole = xs >= x0 && xs + nb <= x1, last = it.y < 0;
+        float* part = last ? reinterpret_cast<float*>(st_ptr) : ws_warp + w * PART;
+        if (!whole && lane == 0) s_piece[2 * w + (x0 < xs)] = 2 * pair + last;
+        bf16* out = a.out + (size_t)pair * G * HD;
+        // eu = 0: no block was read
+        const float unit = eu ? __uint_as_float((uint32_t)(eu - (int)kShift) << 23) : 0.f;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+          for (int sh = 4; sh < 32; sh <<= 1) l2[hh] += __shfl_xor_sync(0xffffffffu, l2[hh], sh);
+          l2[hh] *= 1.f / (1 << (int)kShift);
+          const int head = 2 * t + hh;
+          if (head < G) {
+            const float f = whole ? (l2[hh] == 0.f ? 0.f : unit / l2[hh]) : unit;
+            if (!whole && g == 0) {
+              part[G * HD + head] = m2[hh];
+              part[G * HD + G + head] = l2[hh];
+            }
+#pragma unroll
+            for (int d = 0; d < KS; ++d) {
+              const int at = head * HD + 16 * d + 2 * g;
+              if (whole)
+                *reinterpret_cast<uint32_t*>(out + at) = pack_bf16(o[d][hh] * f, o[d][hh + 2] * f);
+              else
+                *reinterpret_cast<float2*>(part + at) =
+                    make_float2(o[d][hh] * f, o[d][hh + 2] * f);
+            }
+          }
+        }
+      }
+      if (it.y < 0) break;
+      pair = it.y;
+      const int b = pair / H, h = pair - b * H;
+      len = lens[b];
+      lo = a.window ? max(0, len - a.window) : 0;
+      eu = 0;
+      m2[0] = m2[1] = -INFINITY;
+      c2[0] = c2[1] = INFINITY;
+      l2[0] = l2[1] = 0.f;
+#pragma unroll
+      for (int d = 0; d < KS; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+      // Q^T fragments: lane (g, t) holds head g; k-step 4c + i of 64-dim chunk
+      // c pairs dims 64c + 16t + 4i + {0, 1} and {2, 3}, as the K loads do
       uint2 raw[KS];
       uint32_t mx = 0;
       const bf16* qr = a.q + b * a.qs_b + (int64_t)(h * G + min(g, G - 1)) * a.qs_h;
@@ -251,230 +326,338 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attend_kernel(const Kv8Attend
       hs[1] = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
     }
 
-    float m2[2] = {-INFINITY, -INFINITY}, l2[2] = {0.f, 0.f};
-    float o[KS][4];
+    const int j = it.x;
+    ok = mbar_wait_warp(full + s, ph, kPolls);
+    if (ok && j >= 0) {
+      const uint32_t ka = st_base + s * L::STAGE, va = ka + L::MAT;
+      const int p0 = j * kKv8Block;
+      const bool edge = p0 < lo || p0 + kKv8Block > len;
+      if (edge) {
+        // rows outside [lo, len) get weight 0; zero their V codes, so that
+        // whatever they hold cannot turn 0 * v into NaN
+        uint8_t* vt = st_ptr + s * L::STAGE + L::MAT;
+        for (int e = lane; e < kKv8Block * (HD / 16); e += 32) {
+          const int r = e / (HD / 16), c = e - r * (HD / 16);
+          if (p0 + r < lo || p0 + r >= len)
+            *reinterpret_cast<uint4*>(vt + tile_off<HD>(r, c)) = make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+      }
+      // S^T: key 8i + perm(g); sa rows i = 0 (c0, c1) and 1 (c2, c3), sb 2 and 3
+      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+      const int pg = perm<HD>(g);
 #pragma unroll
-    for (int d = 0; d < KS; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+      for (int c = 0; c < (HD + 63) / 64; ++c) {
+        uint32_t kw[4][4];
+        const bool wide = c < HD / 64;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (wide)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(kw[i][0]), "=r"(kw[i][1]), "=r"(kw[i][2]), "=r"(kw[i][3])
+                         : "r"(ka + tile_off<HD>(8 * i + pg, 4 * c + t)));
+          else
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                         : "=r"(kw[i][0]), "=r"(kw[i][1])
+                         : "r"(ka + tile_off<HD>(8 * i + pg, 8 + (t >> 1)) + 8 * (t & 1)));
+        }
+#pragma unroll
+        for (int i = 0; i < (wide ? 4 : 2); ++i) {
+          const int k = 4 * c + i;
+          mma16816_f16(sa, kv8_f16x2(kw[0][i]), kv8_f16x2(kw[1][i]), kv8_f16x2(kw[0][i] >> 16),
+                       kv8_f16x2(kw[1][i] >> 16), qf[k][0], qf[k][1]);
+          mma16816_f16(sb, kv8_f16x2(kw[2][i]), kv8_f16x2(kw[3][i]), kv8_f16x2(kw[2][i] >> 16),
+                       kv8_f16x2(kw[3][i] >> 16), qf[k][0], qf[k][1]);
+        }
+      }
+      // V's scale against O's unit
+      const int ev = (uint32_t)it.w >> 23;
+      if (eu == 0) eu = abs(ev - 127) <= kFar ? ev : 127 + (int)kShift;
+      if (abs(ev - eu) > kFar) {       // from here on O in plain units
+        const float f = __uint_as_float((uint32_t)(eu - (int)kShift) << 23);
+#pragma unroll
+        for (int d = 0; d < KS; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[d][i] *= f;
+        eu = 127 + (int)kShift;
+      }
+      const bool near = abs(ev - eu) <= kNear;
+      const float lr = near ? (float)(ev - eu) : 0.f;
 
-    for (; ok && n < items && x0 + w + NW * n < xn; ++n) {
-      const float ksc = ks, vsc = vs;
-      const int u = meta[s].x, j = meta[s].y;
-      const int s1 = s + 1 == NST ? 0 : s + 1;
-      if (n + 1 < items) load_scales(s1);
-      ok = mbar_wait_warp(full + s, ph);
-      if (ok && u >= 0) {
-        const uint32_t ka = st_base + s * L::STAGE, va = ka + L::MAT;
-        const int p0 = j * kKv8Block;
-        const bool edge = p0 < lo || p0 + kKv8Block > len;
-        if (edge) {
-          // rows outside [lo, len) get weight 0; zero their V codes, so that
-          // whatever they hold cannot turn 0 * v into NaN
-          uint8_t* vt = st_ptr + s * L::STAGE + L::MAT;
-          for (int e = lane; e < kKv8Block * (HD / 16); e += 32) {
-            const int r = e / (HD / 16), c = e - r * (HD / 16);
-            if (p0 + r < lo || p0 + r >= len)
-              *reinterpret_cast<uint4*>(vt + group_off<HD>(r >> 2) + (r & 3) * HD + 16 * c) =
-                  make_uint4(0, 0, 0, 0);
-          }
-          __syncwarp();
-        }
-        // S^T: key 4g + i; sa rows i = 0 (c0, c1) and 1 (c2, c3), sb 2 and 3
-        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t kr = ka + group_off<HD>(g);
+      const float ks = __int_as_float(it.z), f0 = hs[0] * ks, f1 = hs[1] * ks;
+      const float x[4][2] = {{sa[0], sa[1]}, {sa[2], sa[3]}, {sb[0], sb[1]}, {sb[2], sb[3]}};
+      float p[4][2], top = -INFINITY;
+      auto scores = [&]() {
+        const float a0 = c2[0] + lr, a1 = c2[1] + lr;
 #pragma unroll
-        for (int c = 0; c < (HD + 63) / 64; ++c) {
-          uint32_t kw[4][4];
-          const bool wide = c < HD / 64;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (wide)
-              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(kw[i][0]), "=r"(kw[i][1]), "=r"(kw[i][2]), "=r"(kw[i][3])
-                           : "r"(kr + i * HD + 64 * c + 16 * t));
-            else
-              asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                           : "=r"(kw[i][0]), "=r"(kw[i][1])
-                           : "r"(kr + i * HD + 64 * c + 8 * t));
-          }
-#pragma unroll
-          for (int i = 0; i < (wide ? 4 : 2); ++i) {
-            const int k = 4 * c + i;
-            mma16816_f16(sa, kv8_f16x2(kw[0][i]), kv8_f16x2(kw[1][i]), kv8_f16x2(kw[0][i] >> 16),
-                         kv8_f16x2(kw[1][i] >> 16), qf[k][0], qf[k][1]);
-            mma16816_f16(sb, kv8_f16x2(kw[2][i]), kv8_f16x2(kw[3][i]), kv8_f16x2(kw[2][i] >> 16),
-                         kv8_f16x2(kw[3][i] >> 16), qf[k][0], qf[k][1]);
+        for (int i = 0; i < 4; ++i) {
+          p[i][0] = fmaf(x[i][0], f0, a0);
+          p[i][1] = fmaf(x[i][1], f1, a1);
+          if (edge) {
+            const int pos = p0 + 8 * i + pg;
+            if (pos < lo || pos >= len) p[i][0] = p[i][1] = -INFINITY;
           }
         }
-        const float f0 = hs[0] * ksc, f1 = hs[1] * ksc;
-        float sc[4][2] = {{sa[0] * f0, sa[1] * f1}, {sa[2] * f0, sa[3] * f1},
-                          {sb[0] * f0, sb[1] * f1}, {sb[2] * f0, sb[3] * f1}};
-        if (edge) {
+      };
+      scores();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int p = p0 + 4 * g + i;
-            if (p < lo || p >= len) sc[i][0] = sc[i][1] = -INFINITY;
-          }
-        }
-        float corr[2];
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(p[i][0], p[i][1]));
+      if (__any_sync(0xffffffffu, top > kShift + kSlack + lr)) {
+        // a new reference max per head
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          float mx = fmaxf(fmaxf(sc[0][hh], sc[1][hh]), fmaxf(sc[2][hh], sc[3][hh]));
+          const float f = hh ? f1 : f0;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (p[i][hh] != -INFINITY) mx = fmaxf(mx, x[i][hh] * f);
 #pragma unroll
           for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
           const float mn = fmaxf(m2[hh], mx);
-          corr[hh] = mn == -INFINITY ? 1.f : ex2(m2[hh] - mn);
-          const float mm = mn == -INFINITY ? 0.f : mn - kShift;
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sc[i][hh] = ex2(sc[i][hh] - mm);
-            sum += sc[i][hh];
-          }
-          l2[hh] = l2[hh] * corr[hh] + sum;      // of this lane's keys
+          const float corr = mn == -INFINITY ? 1.f : ex2(m2[hh] - mn);
           m2[hh] = mn;
-        }
-        uint32_t pb[4];
+          c2[hh] = kShift - mn;
+          l2[hh] *= corr;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2 v = __floats2half2_rn(sc[i][0], sc[i][1]);
-          pb[i] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&v));
+          for (int d = 0; d < KS; ++d) {
+            o[d][hh] *= corr;
+            o[d][hh + 2] *= corr;
+          }
         }
-        // O^T: rows g and g + 8 of 16-dim block d are dims 16d + 2g, 16d + 2g + 1
-        const uint32_t vr = va + group_off<HD>(lane & 7) + (lane >> 3) * HD;
+        scores();
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i][0] = ex2(p[i][0]);
+        p[i][1] = ex2(p[i][1]);
+      }
+      const float ir = near ? __uint_as_float((uint32_t)(127 + eu - ev) << 23) : 1.f;
+      l2[0] = fmaf((p[0][0] + p[1][0]) + (p[2][0] + p[3][0]), ir, l2[0]);   // this lane's keys
+      l2[1] = fmaf((p[0][1] + p[1][1]) + (p[2][1] + p[3][1]), ir, l2[1]);
+      uint32_t pb[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 v = __floats2half2_rn(p[i][0], p[i][1]);
+        pb[i] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&v));
+      }
+      // O^T: rows g and g + 8 of 16-dim block d are dims 16d + 2g, 16d + 2g + 1
+      const int vr = 8 * (lane >> 3) + perm<HD>(lane & 7);
+      auto add_pv = [&](int d, float (&acc)[4]) {
+        uint32_t r[4];
+        ldsm_x4_t(va + tile_off<HD>(vr, d), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = __byte_perm(r[i], 0, 0x3120);
+        mma16816_f16(acc, kv8_f16x2(r[0]), kv8_f16x2(r[0] >> 16), kv8_f16x2(r[1]),
+                     kv8_f16x2(r[1] >> 16), pb[0], pb[1]);
+        mma16816_f16(acc, kv8_f16x2(r[2]), kv8_f16x2(r[2] >> 16), kv8_f16x2(r[3]),
+                     kv8_f16x2(r[3] >> 16), pb[2], pb[3]);
+      };
+      if (near) {
+#pragma unroll
+        for (int d = 0; d < KS; ++d) add_pv(d, o[d]);
+      } else {
+        const float f = __uint_as_float((uint32_t)ev << 23) * __uint_as_float((uint32_t)(254 - eu) << 23);
 #pragma unroll
         for (int d = 0; d < KS; ++d) {
-          uint32_t r[4];
-          ldsm_x4_t(vr + 16 * d, r[0], r[1], r[2], r[3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) r[i] = __byte_perm(r[i], 0, 0x3120);
           float tt[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816_f16(tt, kv8_f16x2(r[0]), kv8_f16x2(r[0] >> 16), kv8_f16x2(r[1]),
-                       kv8_f16x2(r[1] >> 16), pb[0], pb[1]);
-          mma16816_f16(tt, kv8_f16x2(r[2]), kv8_f16x2(r[2] >> 16), kv8_f16x2(r[3]),
-                       kv8_f16x2(r[3] >> 16), pb[2], pb[3]);
-          o[d][0] = fmaf(tt[0], vsc, o[d][0] * corr[0]);
-          o[d][1] = fmaf(tt[1], vsc, o[d][1] * corr[1]);
-          o[d][2] = fmaf(tt[2], vsc, o[d][2] * corr[0]);
-          o[d][3] = fmaf(tt[3], vsc, o[d][3] * corr[1]);
-        }
-        if (edge) fence_proxy_async_smem();
-      }
-      __syncwarp();                    // the stage has been read
-      if (ok && n + NST < items) issue(n + NST, s);
-      s = s1;
-      if (s == 0) ph ^= 1;
-    }
-
-    // the pair's state in this thread block: the warps' states joined
+          add_pv(d, tt);
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll
-      for (int sh = 4; sh < 32; sh <<= 1) l2[hh] += __shfl_xor_sync(0xffffffffu, l2[hh], sh);
-      const int head = 2 * t + hh;
-      if (head < G) {
-        float* ws = comb + (w * G + head) * (HD + 2);
-        if (g == 0) {
-          ws[0] = m2[hh];
-          ws[1] = l2[hh];
-        }
-#pragma unroll
-        for (int d = 0; d < KS; ++d)
-          *reinterpret_cast<float2*>(ws + 2 + 16 * d + 2 * g) = make_float2(o[d][hh], o[d][hh + 2]);
-      }
-    }
-    __syncthreads();
-    const bool whole = x == xs && xn == xe;
-    float* part = reinterpret_cast<float*>((char*)a.ws + prefix_bytes(B)) +
-                  (size_t)(2 * blockIdx.x + (x != x0)) * L::PART;
-    for (int i = tid; i < G * HD; i += kThreads) {
-      const int head = i / HD, d = i - head * HD;
-      const float* cs = comb + head * (HD + 2);
-      float M = -INFINITY, Ls = 0.f, O = 0.f;
-#pragma unroll
-      for (int k = 0; k < NW; ++k) M = fmaxf(M, cs[k * G * (HD + 2)]);
-#pragma unroll
-      for (int k = 0; k < NW; ++k) {
-        const float* ck = cs + k * G * (HD + 2);
-        const float f = ck[0] == -INFINITY ? 0.f : ex2(ck[0] - M);
-        Ls = fmaf(f, ck[1], Ls);
-        O = fmaf(f, ck[2 + d], O);
-      }
-      if (whole) {
-        a.out[((size_t)b * H + h) * G * HD + i] = __float2bfloat16_rn(Ls == 0.f ? 0.f : O / Ls);
-      } else {
-        part[2 * G + i] = O;
-        if (d == 0) {
-          part[head] = M;
-          part[G + head] = Ls;
+          for (int i = 0; i < 4; ++i) o[d][i] = fmaf(tt[i], f, o[d][i]);
         }
       }
+      if (edge) fence_proxy_async_smem();
     }
-    __syncthreads();
-    x = xn;
+    __syncwarp();                      // the stage has been read
+    if (!ok) break;
+    if (n + NST < items) issue(n + NST, s);
+    if (++s == NST) {
+      s = 0;
+      ph ^= 1;
+    }
   }
   // after a timeout, wait (bounded) for the copies still in flight
   if (!ok) {
     if (lane == 0) atomicOr(a.err, ERRBIT_TIMEOUT);
     for (int m = n; m < min(items, n + NST); ++m)
-      if (!mbar_wait_warp(full + m % NST, (uint32_t)((m / NST) & 1))) break;
+      if (!mbar_wait_warp(full + m % NST, (uint32_t)((m / NST) & 1), kPolls)) break;
+  }
+  __syncthreads();
+
+  // ---- pieces of this thread block: one (pair, head) per warp in turn -------
+  constexpr int NV = (HD + 127) / 128;
+  const int id = lane < 2 * NW ? s_piece[lane] : -1;   // lane 2w + slot
+  const float* mine = nullptr;                         // and where that piece is
+  if (id >= 0)
+    mine = id & 1 ? reinterpret_cast<const float*>(stages + (size_t)(lane >> 1) * NST * L::STAGE)
+                  : ws_warp + (lane >> 1) * PART;
+  unsigned left = __ballot_sync(0xffffffffu, id >= 0);
+  for (int task = 0; left;) {
+    const int pr = __shfl_sync(0xffffffffu, id >> 1, __ffs(left) - 1);
+    const bool in = id >= 0 && id >> 1 == pr;
+    const unsigned of = __ballot_sync(0xffffffffu, in);
+    left &= ~of;
+    int nb;
+    const int xs = start_of(pr, &nb);
+    const bool whole = xs >= X0 && xs + nb <= X1;
+    float* part = ws_block + (size_t)(2 * blockIdx.x + (X0 < xs)) * PART;
+    for (int head = 0; head < G; ++head, ++task) {
+      if (task % NW != w) continue;
+      const float m = in ? mine[G * HD + head] : -INFINITY;
+      const float l = in ? mine[G * HD + G + head] : 0.f;
+      const float M = warp_max(m), f = m == -INFINITY ? 0.f : ex2(m - M), Ls = warp_sum(l * f);
+      float4 O[NV];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) O[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (unsigned r = of; r; r &= r - 1) {
+        const int k = __ffs(r) - 1;
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        const float* q = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), k)) + head * HD;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int d = 4 * (lane + 32 * v);
+          if (d < HD) {
+            const float4 y = *reinterpret_cast<const float4*>(q + d);
+            O[v].x = fmaf(fk, y.x, O[v].x);
+            O[v].y = fmaf(fk, y.y, O[v].y);
+            O[v].z = fmaf(fk, y.z, O[v].z);
+            O[v].w = fmaf(fk, y.w, O[v].w);
+          }
+        }
+      }
+      const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int d = 4 * (lane + 32 * v);
+        if (d >= HD) continue;
+        if (whole)
+          *reinterpret_cast<uint2*>(a.out + ((size_t)pr * G + head) * HD + d) =
+              make_uint2(pack_bf16(O[v].x * inv, O[v].y * inv), pack_bf16(O[v].z * inv, O[v].w * inv));
+        else
+          *reinterpret_cast<float4*>(part + head * HD + d) = O[v];
+      }
+      if (!whole && lane == 0) {
+        part[G * HD + head] = M;
+        part[G * HD + G + head] = Ls;
+      }
+    }
   }
 }
 
-// Joins the partials of pairs cut between thread blocks: one block per
-// (query head, pair), warps over the partials.
-template <int HD>
-__global__ void __launch_bounds__(128) kv8_merge_kernel(const Kv8AttendArgs a, int grid) {
-  constexpr int W = 4, D = HD / 32;
-  __shared__ float sm[W], sl[W], so[W][HD];
+// Joins the pieces of pairs cut between thread blocks, in order: one block per
+// (pair, `heads` of its query heads), blockDim.y = heads x splits warps, each
+// with an equal share of one head's pieces, four at a time (one L2 round
+// trip), joined through shared memory.
+template <int HD, int G>
+__global__ void kv8_merge_kernel(const Kv8AttendArgs a, int grid, int heads) {
+  constexpr int kMaxW = 16, NV = (HD + 127) / 128, U = 4, PART = kPart<HD, G>;
+  __shared__ float sm[kMaxW], sl[kMaxW];
+  __shared__ int si[kMaxW][3];
+  __shared__ __align__(16) float so[kMaxW][HD];
+  // The lengths were written before the attention kernel started, so they
+  // may be read before it ends.
+  const int H = a.c.Hkv, w = threadIdx.y, lane = threadIdx.x;
+  const int pair = blockIdx.x, b = pair / H, h = pair - b * H;
+  // blocks before sequence b, of it, and in all
+  int v3[3] = {0, 0, 0};
+  for (int i = 32 * w + lane; i < a.B; i += 32 * blockDim.y) {
+    const int n = visible_blocks(a, i);
+    v3[2] += n;
+    if (i < b) v3[0] += n;
+    if (i == b) v3[1] = n;
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    v3[k] = __reduce_add_sync(0xffffffffu, v3[k]);
+    if (lane == 0) si[w][k] = v3[k];
+  }
+  __syncthreads();
+  int p0 = 0, nb = 0, total = 0;
+  for (int i = 0; i < (int)blockDim.y; ++i) {
+    p0 += si[i][0];
+    nb += si[i][1];
+    total += si[i][2];
+  }
+  total *= H;
   pdl_wait();
   pdl_trigger();
-  const int G = a.G, H = a.c.Hkv, B = a.B;
-  const int head = blockIdx.x % G, pair = blockIdx.x / G, b = pair / H, h = pair - b * H;
-  const int* pre = reinterpret_cast<const int*>(a.ws);
-  const int p0 = pre[b], nb = pre[b + 1] - p0;
   if (nb == 0) return;
-  const int per = run_blocks(pre[B] * H, grid);
+  const int per = (total + grid - 1) / grid;
   const int xs = p0 * H + h * nb, c0 = xs / per, c1 = (xs + nb - 1) / per;
-  if (c0 == c1) return;                // finished in place
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float* parts = reinterpret_cast<const float*>((const char*)a.ws + prefix_bytes(B));
-  float M = -INFINITY, Ls = 0.f, O[D];
+  if (c0 == c1) return;                // finished in one thread block
+  const int SP = blockDim.y / heads;
+  const int head = blockIdx.y * heads + w / SP, sp = w % SP;
+  const float* parts = reinterpret_cast<const float*>(a.ws);
+  const int cnt = c1 - c0 + 1, share = (cnt + SP - 1) / SP;
+  const int d0 = c0 + sp * share, d1 = min(c1 + 1, d0 + share);
+  float M = -INFINITY, Ls = 0.f;
+  float4 O[NV];
 #pragma unroll
-  for (int d = 0; d < D; ++d) O[d] = 0.f;
-#pragma unroll 2
-  for (int c = c0 + w; c <= c1; c += W) {
-    // a thread block's first slot holds the pair its run starts in
-    const float* p = parts + (size_t)(2 * c + (c * per < xs)) * (G * (HD + 2));
-    const float m = p[head], l = p[G + head];
-    float v[D];
+  for (int v = 0; v < NV; ++v) O[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int e = d0; e < d1; e += U) {
+    float m[U], l[U];
+    float4 x[U][NV];
 #pragma unroll
-    for (int d = 0; d < D; ++d) v[d] = p[2 * G + head * HD + lane + 32 * d];
-    const float mn = fmaxf(M, m);
-    const float f0 = M == -INFINITY ? 0.f : ex2(M - mn), f1 = m == -INFINITY ? 0.f : ex2(m - mn);
-    Ls = Ls * f0 + l * f1;
+    for (int i = 0; i < U; ++i) {
+      const int c = e + i;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
 #pragma unroll
-    for (int d = 0; d < D; ++d) O[d] = O[d] * f0 + v[d] * f1;
+      for (int v = 0; v < NV; ++v) x[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < d1) {
+        // a thread block's first slot holds the pair it starts in
+        const float* p = parts + (2 * (size_t)c + (c * per < xs)) * PART;
+        m[i] = p[G * HD + head];
+        l[i] = p[G * HD + G + head];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int q = 4 * (lane + 32 * v);
+          if (q < HD) x[i][v] = *reinterpret_cast<const float4*>(p + head * HD + q);
+        }
+      }
+    }
+    float mn = M;
+#pragma unroll
+    for (int i = 0; i < U; ++i) mn = fmaxf(mn, m[i]);
+    const float f0 = M == -INFINITY ? 0.f : ex2(M - mn);
     M = mn;
+    Ls *= f0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      O[v] = make_float4(O[v].x * f0, O[v].y * f0, O[v].z * f0, O[v].w * f0);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const float f = m[i] == -INFINITY ? 0.f : ex2(m[i] - mn);
+      Ls = fmaf(f, l[i], Ls);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        O[v].x = fmaf(f, x[i][v].x, O[v].x);
+        O[v].y = fmaf(f, x[i][v].y, O[v].y);
+        O[v].z = fmaf(f, x[i][v].z, O[v].z);
+        O[v].w = fmaf(f, x[i][v].w, O[v].w);
+      }
+    }
   }
   if (lane == 0) {
     sm[w] = M;
     sl[w] = Ls;
   }
 #pragma unroll
-  for (int d = 0; d < D; ++d) so[w][lane + 32 * d] = O[d];
+  for (int v = 0; v < NV; ++v)
+    if (4 * (lane + 32 * v) < HD) *reinterpret_cast<float4*>(&so[w][4 * (lane + 32 * v)]) = O[v];
   __syncthreads();
-  float MM = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < W; ++k) MM = fmaxf(MM, sm[k]);
-  for (int d = threadIdx.x; d < HD; d += 32 * W) {
-    float L = 0.f, S = 0.f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const float f = sm[k] == -INFINITY ? 0.f : ex2(sm[k] - MM);
-      L = fmaf(f, sl[k], L);
-      S = fmaf(f, so[k][d], S);
+  const int nthr = 32 * blockDim.y;
+  for (int i = w * 32 + lane; i < heads * HD; i += nthr) {
+    const int hh = i / HD, d = i - hh * HD;
+    float MM = -INFINITY, L = 0.f, S = 0.f;
+    for (int k = 0; k < SP; ++k) MM = fmaxf(MM, sm[hh * SP + k]);
+    for (int k = 0; k < SP; ++k) {
+      const float f = sm[hh * SP + k] == -INFINITY ? 0.f : ex2(sm[hh * SP + k] - MM);
+      L = fmaf(f, sl[hh * SP + k], L);
+      S = fmaf(f, so[hh * SP + k][d], S);
     }
-    a.out[((size_t)pair * G + head) * HD + d] = __float2bfloat16_rn(L == 0.f ? 0.f : S / L);
+    a.out[((size_t)pair * G + blockIdx.y * heads) * HD + i] =
+        __float2bfloat16_rn(L == 0.f ? 0.f : S / L);
   }
 }
 
@@ -491,37 +674,52 @@ int attend_grid() {
 }
 
 template <int HD, int G>
-void attend_t(const Kv8AttendArgs& a, cudaStream_t st) {
-  using L = Att<HD, G>;
+void attend_t(const Kv8AttendArgs& a, const Kv8Maps& maps, cudaStream_t st) {
+  using L = Att<HD>;
   const int grid = attend_grid();
   const size_t smem = L::smem(a.B);
   cudaFuncSetAttribute(kv8_attend_kernel<HD, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)smem);
-  launch_k(kv8_attend_kernel<HD, G>, dim3(grid), dim3(kThreads), smem, st, a);
-  launch_k(kv8_merge_kernel<HD>, dim3(a.B * a.c.Hkv * G), dim3(128), 0, st, a, grid);
+  launch_k(kv8_attend_kernel<HD, G>, dim3(grid), dim3(32 * L::NW), smem, st, maps, a);
+  // the fewer pairs, the more pieces each may have
+  const int pairs = a.B * a.c.Hkv;
+  const bool few = pairs <= 64;
+  const int heads = few ? 1 : G, warps = few ? (pairs <= 16 ? 16 : 8) : std::max(8, G);
+  launch_k(kv8_merge_kernel<HD, G>, dim3(pairs, G / heads), dim3(32, warps), 0, st, a, grid, heads);
 }
 
 template <int HD>
-void attend_hd(const Kv8AttendArgs& a, cudaStream_t st) {
+void attend_hd(const Kv8AttendArgs& a, const Kv8Maps& maps, cudaStream_t st) {
   switch (a.G) {
-    case 1: attend_t<HD, 1>(a, st); break;
-    case 2: attend_t<HD, 2>(a, st); break;
-    case 4: attend_t<HD, 4>(a, st); break;
-    default: attend_t<HD, 8>(a, st); break;
+    case 1: attend_t<HD, 1>(a, maps, st); break;
+    case 2: attend_t<HD, 2>(a, maps, st); break;
+    case 4: attend_t<HD, 4>(a, maps, st); break;
+    default: attend_t<HD, 8>(a, maps, st); break;
   }
 }
 
 }  // namespace
 
-size_t kv8_attend_ws(int B, int G, int hd) {
-  return prefix_bytes(B) + (size_t)2 * attend_grid() * G * (hd + 2) * 4;
+size_t kv8_attend_ws(int G, int hd) {
+  const int nw = hd == 64 ? Att<64>::NW : hd == 128 ? Att<128>::NW : Att<160>::NW;
+  return (size_t)(2 + nw) * attend_grid() * ((G * (hd + 2) + 3) & ~3) * sizeof(float);
 }
 
-void launch_kv8_attend(const Kv8AttendArgs& a, cudaStream_t st) {
+bool make_kv8_maps(const Kv8& c, Kv8Maps* m) {
+  const long rows = (long)c.n_pages * c.Hkv * kPage;
+  const int w1 = c.hd == 64 ? 64 : 128;
+  *m = Kv8Maps{};
+  return make_map_bytes(&m->k, c.k, rows, c.hd, w1, kKv8Block) &&
+         make_map_bytes(&m->v, c.v, rows, c.hd, w1, kKv8Block) &&
+         (c.hd != 160 || (make_map_bytes(&m->k2, c.k, rows, c.hd, 32, kKv8Block) &&
+                          make_map_bytes(&m->v2, c.v, rows, c.hd, 32, kKv8Block)));
+}
+
+void launch_kv8_attend(const Kv8AttendArgs& a, const Kv8Maps& maps, cudaStream_t st) {
   switch (a.c.hd) {
-    case 64: attend_hd<64>(a, st); break;
-    case 128: attend_hd<128>(a, st); break;
-    default: attend_hd<160>(a, st); break;
+    case 64: attend_hd<64>(a, maps, st); break;
+    case 128: attend_hd<128>(a, maps, st); break;
+    default: attend_hd<160>(a, maps, st); break;
   }
 }
 

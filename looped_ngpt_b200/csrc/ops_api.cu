@@ -88,12 +88,12 @@ int dory_kv8_workspace_bytes(const dory_kv8* c, int n_q_heads, int64_t* bytes) {
   if (!bytes || n_q_heads < 1 || n_q_heads % c->n_kv_heads) return DORY_ERR_ARG;
   const int G = n_q_heads / c->n_kv_heads;
   if (G != 1 && G != 2 && G != 4 && G != 8) return DORY_ERR_UNSUPPORTED;
-  // block counts are int32, and every sequence has an entry in shared memory
+  // block counts and TMA rows are int32, and every sequence has an entry in shared memory
   if (c->batch > kKv8MaxBatch ||
       (int64_t)c->batch * c->pages_per_seq * 2 * c->n_kv_heads > INT_MAX / 2 ||
-      (int64_t)c->n_pages * 2 * c->n_kv_heads > INT_MAX)
+      (int64_t)c->n_pages * c->n_kv_heads * kPage > INT_MAX)
     return DORY_ERR_UNSUPPORTED;
-  *bytes = (int64_t)kv8_attend_ws(c->batch, G, c->head_dim);
+  *bytes = (int64_t)kv8_attend_ws(G, c->head_dim);
   return DORY_OK;
 }
 
@@ -111,11 +111,12 @@ int dory_kv8_attend(const dory_kv8* c, const void* d_q,
   if (need > ws_bytes) return DORY_ERR_WORKSPACE;
   cudaGetLastError();
   int* err = device_status_word();
-  if (!err) return DORY_ERR_CUDA;
+  Kv8Maps maps;
+  if (!err || !make_kv8_maps(to_kv8(c), &maps)) return DORY_ERR_CUDA;
   launch_kv8_attend(Kv8AttendArgs{to_kv8(c), c->batch, n_q_heads / c->n_kv_heads,
                                   (const bf16*)d_q, q_strides[0], q_strides[1], d_len, window,
                                   scale, (bf16*)d_out, d_ws, err},
-                    (cudaStream_t)stream);
+                    maps, (cudaStream_t)stream);
   return launched();
 }
 

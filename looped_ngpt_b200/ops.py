@@ -198,7 +198,8 @@ class KV8Pages:
                 pos.data_ptr(), None if n is None else n.data_ptr(), st))
 
     def workspace(self, n_q_heads):
-        """A workspace for attend with n_q_heads query heads."""
+        """A workspace for attend with n_q_heads query heads; one
+        call at a time may use it."""
         nb = ctypes.c_int64()
         with torch.cuda.device(self.device):
             check("dory_kv8_workspace_bytes",

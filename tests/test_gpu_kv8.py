@@ -28,6 +28,12 @@ def model():
     return lb.DoryModel(TINY, make_weights(TINY, seed=0), device="cuda:0")
 
 
+@pytest.fixture(autouse=True)
+def no_device_error(model):
+    yield
+    assert model.sync_status() == 0
+
+
 def bf(x):
     """float64 -> the bf16 values a GPU tensor of it holds."""
     return torch.tensor(np.asarray(x), dtype=torch.float32).to(torch.bfloat16)
