@@ -9,8 +9,8 @@
 // u times the kept mass.  Weights and sums are f64: a draw is decided by
 // which side of one of up to V borders u falls, and in f32 those borders are
 // off by more than neighbouring u differ.  (top-p's cutoff compares sums of
-// weights rounded to 2^-46 or so in 64-bit integers, whose order of addition
-// is free.)
+// weights rounded to 2^-43 in 64-bit integers, whose order of addition is
+// free.)
 //
 // One thread-block cluster per row, up to 16 blocks: each keeps a slice of
 // the row in shared memory, read from HBM once, and the blocks exchange
@@ -34,7 +34,8 @@ typedef unsigned long long u64;
 constexpr int kSampThreads = 512, kSW = kSampThreads / 32;
 constexpr int kMaxC = 16;            // blocks per row
 constexpr int kNB = 128;             // bins of a histogram
-constexpr int kGC = 64;              // candidates per block
+constexpr int kRank = 128;           // candidates ranked by comparing each pair
+constexpr int kU = 4;                // logits a thread handles at once
 
 // NaN counts as -inf (never drawn).
 __device__ __forceinline__ float clean(float z) { return z > -INFINITY ? z + 0.f : -INFINITY; }
@@ -54,24 +55,24 @@ __constant__ double kExpTab[16] = {
     0x1.6a09e667f3bcdp+0, 0x1.7a11473eb0187p+0, 0x1.8ace5422aa0dbp+0, 0x1.9c49182a3f090p+0,
     0x1.ae89f995ad3adp+0, 0x1.c199bdd85529cp+0, 0x1.d5818dcfba487p+0, 0x1.ea4afa2a490dap+0};
 
-// e^x for x <= 0, relative error below (8 + |x|) 2^-53: x = (16 n + j) ln2 / 16 + r,
-// |r| <= ln2 / 32, e^x = 2^n 2^(j/16) (Taylor series of e^r to r^6, whose
-// next term is below 2^-50).  0 below -700.  tab: 2^(j/16) in shared memory
-// (16 doubles, one per bank pair).
-__device__ __forceinline__ double exp_neg(double x, const double* tab) {
-  constexpr double kMagic = 0x1.8p52;
-  const double t = fma(x, 16.0 / 0.693147180559945309417, kMagic);
+// 2^(y/16) for y <= 0, relative error below 2^-41 + |y| 2^-53: y = 16 n + j + f,
+// |f| <= 1/2, by 2^n 2^(j/16) and the Taylor series of 2^(f/16) to f^5 (whose
+// next term is below 2^-42).  0 below y = -16000.  tab: 2^(j/16) in shared
+// memory (16 doubles, one per bank pair).  A weight off by 2^-41 moves a
+// border of the running sum by less than the chance 2^-32 of a uniform's
+// falling between.
+__device__ __forceinline__ double exp2_16th(double y, const double* tab) {
+  constexpr double kMagic = 0x1.8p52, c = 0.693147180559945309417 / 16;
+  const double t = y + kMagic, f = y - (t - kMagic);
   const int k = __double2loint(t);
-  const double r = fma(t - kMagic, -0.693147180559945309417 / 16.0, x);
-  double p = fma(r, 1.0 / 720, 1.0 / 120);
-  p = fma(p, r, 1.0 / 24);
-  p = fma(p, r, 1.0 / 6);
-  p = fma(p, r, 0.5);
-  p = fma(p, r, 1.0);
-  p = fma(p, r, 1.0);
+  double p = fma(f, c * c * c * c * c / 120, c * c * c * c / 24);
+  p = fma(p, f, c * c * c / 6);
+  p = fma(p, f, c * c / 2);
+  p = fma(p, f, c);
+  p = fma(p, f, 1.0);
   p *= tab[k & 15];
   const double v = __hiloint2double(__double2hiint(p) + ((k >> 4) << 20), __double2loint(p));
-  return x > -700.0 ? v : 0.0;
+  return y > -16000.0 ? v : 0.0;
 }
 
 template <typename T>
@@ -95,47 +96,65 @@ struct Cand {
   u64 w;
 };
 
-// What the blocks of a row write into each other (index: writer).  A buffer
-// is written again only after a barrier that follows its last read.
-struct Exchange {
-  float max[kMaxC], min[kMaxC];
-  int arg[kMaxC];
-  uint32_t cnt[kMaxC][kNB];
-  u64 mass[kMaxC][kNB];
-  int g_n[kMaxC];
-  float g_min[kMaxC], g_max[kMaxC];
-  Cand g[kMaxC][kGC];
-  int tie;
-  double sum[kMaxC];
-};
-
-struct Local {
-  Exchange ex;
+// Shared memory of a block.  `Fixed`, then, with C blocks per row and slices
+// of `per` logits:
+//   mass  u64 [C][kNB]     histograms, written by the row's blocks (index:
+//                          writer), as everything in `Fixed::ex`
+//   cands Cand [C][gc]     candidates, written likewise
+//   hist  u32 [kSW][2][kNB] histograms of the warps' parts of the slice:
+//                          counts, or (by mass) the low 22 and the upper bits
+//                          of the weights, whose sums over up to 1024 logits
+//                          stay below 2^32 (64-bit atomics on shared memory
+//                          ran 17 times slower); then the own candidates
+//   zs    f32 [per]        the slice
+//   bins  u8 [per]         bin of each logit in the last histogram
+// A buffer that other blocks write is written again only after a barrier that
+// follows its last read.
+struct Fixed {
+  struct {
+    uint32_t max[kMaxC], min[kMaxC];   // integer images
+    int g_n[kMaxC];
+    uint32_t g_min[kMaxC], g_max[kMaxC];
+    int tie;
+    double sum[kMaxC];
+  } ex;
   double tab[16];
-  uint32_t cnt[kNB];
-  u64 mass[kNB];
-  Cand cand[kGC];
-  int n;
-  uint32_t kmin, kmax;
+  u64 bin_mass[kNB];
   // the chosen bin, and count and mass of what lies above it
-  int bin, above;
   u64 mass_above, want;
+  int bin, n;
+  uint32_t kmin, kmax;
   float cut_z;
   int cut_i;
-  float fred[kSW], fred2[kSW];
+  uint32_t ured[2][kSW];
   int ired[kSW];
   double dred[kSW];
-  int pick;
 };
+constexpr int kHistWords = kSW * 2 * kNB;
+static_assert(sizeof(Fixed) % 16 == 0, "what follows is 16-byte aligned");
+
+// Candidates per block: few blocks may send more each.
+__host__ __device__ inline int cand_cap(int C) { return C >= 4 ? 32 : kRank / C; }
+__host__ __device__ inline size_t sample_smem(int C, int per) {
+  return sizeof(Fixed) + (size_t)C * kNB * 8 + (size_t)C * cand_cap(C) * sizeof(Cand) +
+         kHistWords * 4 + (size_t)per * 5;
+}
+static_assert(kRank * sizeof(Cand) <= kHistWords * 4, "candidates fit the histograms' place");
 
 __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, int C, int pw) {
   extern __shared__ __align__(16) uint8_t smraw[];
-  Local& s = *reinterpret_cast<Local*>(smraw);
-  float* zs = reinterpret_cast<float*>(smraw + sizeof(Local));
+  Fixed& s = *reinterpret_cast<Fixed*>(smraw);
+  const int gc = cand_cap(C);
+  u64* ex_mass = reinterpret_cast<u64*>(smraw + sizeof(Fixed));
+  Cand* ex_cand = reinterpret_cast<Cand*>(ex_mass + C * kNB);
+  uint32_t* hist_all = reinterpret_cast<uint32_t*>(ex_cand + C * gc);
+  Cand* own_cand = reinterpret_cast<Cand*>(hist_all);
+  float* zs = reinterpret_cast<float*>(hist_all + kHistWords);
   const int row = blockIdx.x / C, rank = blockIdx.x - row * C;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = kSW * pw, base = rank * per;      // this block's slice
-  const int wbase = w * pw + lane;                  // this thread's first index in it
+  const int i0 = w * pw + lane, i1 = w * pw + pw;   // this thread's part: i0, i0 + 32, ..
+  uint8_t* bins = reinterpret_cast<uint8_t*>(zs + per);
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if (tid < 16) s.tab[tid] = kExpTab[tid];
   pdl_wait();
@@ -149,75 +168,101 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   minp = minp > 0.f ? fminf(minp, 1.f) : 0.f;
   const float uf = a.uniform[row];
 
-  // ---- the slice, its largest (and where) and smallest finite logit --------
-  float zmax = -INFINITY, zmin = INFINITY;
-  int amax = 0x7fffffff;
-#pragma unroll 8
-  for (int i = wbase; i < w * pw + pw; i += 32) {
-    const int gi = base + i;
-    const float v = gi < a.V ? clean(z[gi]) : -INFINITY;
+  // ---- the slice, its largest and smallest finite logit ---------------------
+  // (4-byte copies: rows need no alignment)
+#pragma unroll 4
+  for (int i = i0; i < i1; i += 32) {
+    if (base + i < a.V)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(su32(zs + i)), "l"(z + base + i)
+                   : "memory");
+    else
+      zs[i] = -INFINITY;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  uint32_t kmax = 0, kmin = 0xffffffffu;            // integer images
+#pragma unroll 4
+  for (int i = i0; i < i1; i += 32) {
+    const float v = clean(zs[i]);
     zs[i] = v;
-    if (v > zmax) { zmax = v; amax = gi; }
-    if (v > -INFINITY) zmin = fminf(zmin, v);
+    if (v > -INFINITY) {
+      kmax = max(kmax, key_of(v));
+      kmin = min(kmin, key_of(v));
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float v = __shfl_xor_sync(0xffffffffu, zmax, o);
-    const int i = __shfl_xor_sync(0xffffffffu, amax, o);
-    if (v > zmax || (v == zmax && i < amax)) { zmax = v; amax = i; }
-    zmin = fminf(zmin, __shfl_xor_sync(0xffffffffu, zmin, o));
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  if (lane == 0) {
+    s.ured[0][w] = kmax;
+    s.ured[1][w] = kmin;
   }
-  if (lane == 0) { s.fred[w] = zmax; s.fred2[w] = zmin; s.ired[w] = amax; }
   __syncthreads();
   // every block has started: its shared memory may be written
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (tid < C) {
-#pragma unroll
-    for (int j = 0; j < kSW; ++j) {
-      const float v = s.fred[j];
-      if (j == 0 || v > zmax || (v == zmax && s.ired[j] < amax)) { zmax = v; amax = s.ired[j]; }
-      zmin = j ? fminf(zmin, s.fred2[j]) : s.fred2[0];
+  if (w == 0) {
+    kmax = __reduce_max_sync(0xffffffffu, s.ured[0][lane & (kSW - 1)]);
+    kmin = __reduce_min_sync(0xffffffffu, s.ured[1][lane & (kSW - 1)]);
+    if (lane < C) {
+      put32(&s.ex.max[rank], lane, kmax);
+      put32(&s.ex.min[rank], lane, kmin);
     }
-    put32(&s.ex.max[rank], tid, __float_as_uint(zmax));
-    put32(&s.ex.min[rank], tid, __float_as_uint(zmin));
-    put32(&s.ex.arg[rank], tid, amax);
   }
   cluster_sync_all();
-  float m = -INFINITY, lo = INFINITY;
-  int arg = 0x7fffffff;
-  for (int c = 0; c < C; ++c) {
-    if (s.ex.max[c] > m) { m = s.ex.max[c]; arg = s.ex.arg[c]; }
-    lo = fminf(lo, s.ex.min[c]);
-  }
-  if (m == INFINITY) lo = m;         // only these weigh anything
-  if (m == -INFINITY || greedy) {    // nothing to draw, or nothing to draw for
+  kmax = __reduce_max_sync(0xffffffffu, lane < C ? s.ex.max[lane] : 0u);
+  kmin = __reduce_min_sync(0xffffffffu, lane < C ? s.ex.min[lane] : 0xffffffffu);
+  if (kmax == 0) {                   // nothing to draw
     if (rank == 0 && tid == 0) {
-      a.tokens[row] = m == -INFINITY ? -1 : arg;
-      if (a.logprobs) a.logprobs[row] = m == -INFINITY ? -INFINITY : 0.f;
+      a.tokens[row] = -1;
+      if (a.logprobs) a.logprobs[row] = -INFINITY;
+    }
+    return;
+  }
+  const float m = key_float(kmax);
+  float lo = m == INFINITY ? m : key_float(kmin);   // beside +inf nothing weighs anything
+  if (greedy) {
+    // the lowest index of the largest logit, in the first block that has it
+    const unsigned has = __ballot_sync(0xffffffffu, lane < C && s.ex.max[lane] == kmax);
+    if (rank != __ffs(has) - 1) return;
+    uint32_t at = 0xffffffffu;
+    for (int i = i0; i < i1; i += 32)
+      if (zs[i] == m) at = min(at, (uint32_t)i);
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (lane == 0) s.ured[0][w] = at;
+    __syncthreads();
+    at = __reduce_min_sync(0xffffffffu, s.ured[0][lane & (kSW - 1)]);
+    if (tid == 0) {
+      a.tokens[row] = base + at;
+      if (a.logprobs) a.logprobs[row] = 0.f;
     }
     return;
   }
   const double inv_t = 1.0 / (double)T, md = (double)m;
+  const double rate = inv_t * (16 / 0.693147180559945309417);
+  // (free of branches, so that kU of them overlap; -inf weighs 0)
   auto weight = [&](float v) -> double {
-    const double x = ((double)v - md) * inv_t;
-    return v == m ? 1.0 : exp_neg(x, s.tab);
+    const double x = exp2_16th(((double)v - md) * rate, s.tab);
+    return v == m ? 1.0 : x;
   };
-  // weights as integers: V of them add up to less than 2^63
-  const double unit = (double)(1ull << (62 - (32 - __clz(a.V))));
-  auto fixed = [&](float v) -> u64 { return __double2ull_rn(weight(v) * unit); };
+  // weights as integers of 43 bits, nearest (adding 2^52 leaves them in the
+  // low bits of the double)
+  auto fixed = [&](float v) -> u64 {
+    return (u64)__double_as_longlong(fma(weight(v), 0x1p43, 0x1p52)) & 0xfffffffffffffull;
+  };
 
   // kept: z > cz, or z == cz and index <= ci
   float cz = -INFINITY;
   int ci = -1;
   if (minp > 0.f) {
     // least logit with weight >= min_p: 32-way search of the integer images
-    uint32_t l = key_of(lo), h = key_of(m);
+    uint32_t l = key_of(lo), h = kmax;
     while (l < h) {
       const uint32_t step = (h - l) / 32 + 1;
       const uint32_t p = l + min(h - l, step * lane);
       const unsigned ok = __ballot_sync(0xffffffffu, weight(key_float(p)) >= (double)minp);
       const int f = ok ? __ffs(ok) - 1 : 32;          // lanes f.. hold
-      if (f == 0) { h = l; break; }
+      if (f == 0) {
+        h = l;
+        break;
+      }
       const uint32_t nl = l + min(h - l, step * (f - 1)) + 1;
       if (f < 32) h = l + min(h - l, step * f);
       l = nl;
@@ -230,84 +275,100 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   // ---- one cutoff: by count (top-k) or by mass (top-p) ----------------------
   auto select = [&](const bool by_mass) {
     float hi = m, low = lo;
-    int above = 0;
-    u64 mass_above = 0, want = 0;
+    // below m - 31 T integer weights are 0
+    if (by_mass) low = fmaxf(low, m - 31.f * T);
+    low = fminf(low, hi);
+    u64 mass_above = 0, want = 0;      // weights, or logits, before and up to the cutoff
     for (int level = 0;; ++level) {
-      // histogram of the kept logits in [low, hi]; equal ones need none
+      // histogram of the kept logits in [low, hi]
       const bool flat = low == hi;
-      const double sc = flat ? 0.0 : (double)kNB / ((double)hi - (double)low);
-      auto bin_of = [&](float v) {
-        return flat ? 0 : min((int)(((double)hi - (double)v) * sc), kNB - 1);
-      };
+      const double hd = (double)hi, sc = flat ? 0.0 : (double)kNB / (hd - (double)low);
       auto in_range = [&](float v, int i) {
         return v <= hi && v >= low && (v > cz || (v == cz && base + i <= ci));
       };
       __syncthreads();
-      for (int i = tid; i < kNB; i += kSampThreads) { s.cnt[i] = 0; s.mass[i] = 0; }
-      if (tid == 0) { s.n = 0; s.kmin = 0xffffffffu; s.kmax = 0; }
-      __syncthreads();
-      for (int i = wbase; i < w * pw + pw; i += 32) {
-        const float v = zs[i];
-        if (v > -INFINITY && in_range(v, i)) {
-          const int bn = bin_of(v);
-          atomicAdd(&s.cnt[bn], 1u);
-          if (by_mass) {
-            const u64 f = fixed(v);
-            if (f) atomicAdd(&s.mass[bn], f);
-          }
-        }
+      for (int i = tid; i < kHistWords; i += kSampThreads) hist_all[i] = 0;
+      if (tid == 0) {
+        s.n = 0;
+        s.kmin = 0xffffffffu;
+        s.kmax = 0;
       }
       __syncthreads();
-      for (int i = tid; i < C * kNB; i += kSampThreads) {
-        const int c = i / kNB, bn = i - c * kNB;
-        put32(&s.ex.cnt[rank][bn], c, s.cnt[bn]);
-        if (by_mass) put64(&s.ex.mass[rank][bn], c, s.mass[bn]);
+      uint32_t* hist = hist_all + w * 2 * kNB;
+      for (int ib = i0; ib < i1; ib += 32 * kU) {
+        float v[kU];
+        bool in[kU], any = false;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int i = ib + 32 * u;
+          v[u] = i < i1 ? zs[i] : -INFINITY;
+          in[u] = v[u] > -INFINITY && in_range(v[u], i);
+          any |= in[u];
+        }
+        if (!__any_sync(0xffffffffu, any)) continue;
+        int bn[kU];
+        u64 f[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          // bin of (hi - v) sc, rounded (monotone; the ends fall into the
+          // first and the last bin)
+          const int q = __double2loint(fma(hd - (double)v[u], sc, 0x1.8p52 - 0.5));
+          bn[u] = flat ? 0 : max(0, min(q, kNB - 1));
+          f[u] = by_mass ? fixed(v[u]) : 1;
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (in[u]) {
+            const uint32_t f0 = (uint32_t)f[u] & 0x3fffffu, f1 = (uint32_t)(f[u] >> 22);
+            bins[ib + 32 * u] = bn[u];
+            if (f0) atomicAdd(hist + bn[u], f0);
+            if (f1) atomicAdd(hist + kNB + bn[u], f1);
+          }
+      }
+      __syncthreads();
+      if (tid < kNB) {
+        u64 f0 = 0, f1 = 0;
+#pragma unroll
+        for (int j = 0; j < kSW; ++j) {
+          f0 += hist_all[j * 2 * kNB + tid];
+          f1 += hist_all[j * 2 * kNB + kNB + tid];
+        }
+        const u64 f = f0 + (f1 << 22);
+        for (int c = 0; c < C; ++c) put64(ex_mass + rank * kNB + tid, c, f);
       }
       cluster_sync_all();
       if (tid < kNB) {
-        uint32_t n = 0;
         u64 f = 0;
-        for (int c = 0; c < C; ++c) {
-          n += s.ex.cnt[c][tid];
-          if (by_mass) f += s.ex.mass[c][tid];
-        }
-        s.cnt[tid] = n;
-        s.mass[tid] = f;
+        for (int c = 0; c < C; ++c) f += ex_mass[c * kNB + tid];
+        s.bin_mass[tid] = f;
       }
       __syncthreads();
       if (w == 0) {
         // lane l holds bins 4l .. 4l + 3
         constexpr int Q = kNB / 32;
-        int n = 0;
         u64 f = 0;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) { n += s.cnt[Q * lane + q]; f += s.mass[Q * lane + q]; }
-        int ni = n;
+        for (int q = 0; q < Q; ++q) f += s.bin_mass[Q * lane + q];
         u64 fi = f;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, ni, o);
           const u64 x = __shfl_up_sync(0xffffffffu, fi, o);
-          if (lane >= o) { ni += y; fi += x; }
+          if (lane >= o) fi += x;
         }
-        if (by_mass && level == 0)
-          want = max((u64)1, (u64)ceil(fmax((double)topp, 0.0) *
-                                       (double)__shfl_sync(0xffffffffu, fi, 31)));
-        int an = above + ni - n;
+        if (level == 0)
+          want = by_mass ? max((u64)1, (u64)ceil(fmax((double)topp, 0.0) *
+                                                 (double)__shfl_sync(0xffffffffu, fi, 31)))
+                         : (u64)k;
         u64 af = mass_above + fi - f;
-        const bool hit = by_mass ? mass_above + fi >= want : above + ni >= k;
-        const unsigned bal = __ballot_sync(0xffffffffu, hit);
+        const unsigned bal = __ballot_sync(0xffffffffu, mass_above + fi >= want);
         if (lane == (bal ? __ffs(bal) - 1 : 31)) {
           int bn = -1;
-          if (bal) {
+          if (bal)
             for (bn = Q * lane; bn < Q * lane + Q - 1; ++bn) {
-              if (by_mass ? af + s.mass[bn] >= want : an + (int)s.cnt[bn] >= k) break;
-              an += s.cnt[bn];
-              af += s.mass[bn];
+              if (af + s.bin_mass[bn] >= want) break;
+              af += s.bin_mass[bn];
             }
-          }
           s.bin = bn;                   // -1: fewer than k are kept
-          s.above = an;
           s.mass_above = af;
           s.want = want;
         }
@@ -318,65 +379,80 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
         cluster_sync_all();             // the histograms have been read
         return;
       }
-      above = s.above;
       mass_above = s.mass_above;
       want = s.want;
       // the bin's logits
-      uint32_t kmin = 0xffffffffu, kmax = 0;
-      for (int i = wbase; i < w * pw + pw; i += 32) {
+      uint32_t bmin = 0xffffffffu, bmax = 0;
+#pragma unroll 4
+      for (int i = i0; i < i1; i += 32) {
         const float v = zs[i];
-        if (v > -INFINITY && in_range(v, i) && bin_of(v) == bin) {
-          const int at = atomicAdd(&s.n, 1);
-          if (at < kGC) s.cand[at] = Cand{v, base + i, by_mass ? fixed(v) : 0};
-          kmin = min(kmin, key_of(v));
-          kmax = max(kmax, key_of(v));
+        const bool hit = v > -INFINITY && in_range(v, i) && bins[i] == bin;
+        const unsigned bal = __ballot_sync(0xffffffffu, hit);
+        if (!bal) continue;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&s.n, __popc(bal));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(bal & ((1u << lane) - 1));
+        if (hit) {
+          if (at < gc) own_cand[at] = Cand{v, base + i, by_mass ? fixed(v) : 1};
+          bmin = min(bmin, key_of(v));
+          bmax = max(bmax, key_of(v));
         }
       }
-      kmin = __reduce_min_sync(0xffffffffu, kmin);
-      kmax = __reduce_max_sync(0xffffffffu, kmax);
-      if (lane == 0) { atomicMin(&s.kmin, kmin); atomicMax(&s.kmax, kmax); }
+      bmin = __reduce_min_sync(0xffffffffu, bmin);
+      bmax = __reduce_max_sync(0xffffffffu, bmax);
+      if (lane == 0 && bmax) {
+        atomicMin(&s.kmin, bmin);
+        atomicMax(&s.kmax, bmax);
+      }
       __syncthreads();
       const int own = s.n;
       if (tid < C) {
         put32(&s.ex.g_n[rank], tid, own);
-        put32(&s.ex.g_min[rank], tid, __float_as_uint(own ? key_float(s.kmin) : INFINITY));
-        put32(&s.ex.g_max[rank], tid, __float_as_uint(own ? key_float(s.kmax) : -INFINITY));
+        put32(&s.ex.g_min[rank], tid, s.kmin);
+        put32(&s.ex.g_max[rank], tid, s.kmax);
       }
-      const int send = min(own, kGC);
+      const int send = min(own, gc);
       for (int i = tid; i < C * send; i += kSampThreads) {
         const int c = i / send, j = i - c * send;
-        put32(&s.ex.g[rank][j].z, c, __float_as_uint(s.cand[j].z));
-        put32(&s.ex.g[rank][j].i, c, s.cand[j].i);
-        put64(&s.ex.g[rank][j].w, c, s.cand[j].w);
+        const Cand x = own_cand[j];
+        Cand* to = ex_cand + rank * gc + j;
+        put32(&to->z, c, __float_as_uint(x.z));
+        put32(&to->i, c, x.i);
+        put64(&to->w, c, x.w);
       }
       cluster_sync_all();
-      bool fits = true;
-      int total = 0;
-      low = INFINITY;
-      hi = -INFINITY;
-      for (int c = 0; c < C; ++c) {
-        fits &= s.ex.g_n[c] <= kGC;
-        total += s.ex.g_n[c];
-        low = fminf(low, s.ex.g_min[c]);
-        hi = fmaxf(hi, s.ex.g_max[c]);
-      }
-      if (fits) {
-        // rank each candidate; the cutoff is the last one kept
-        for (int e = tid; e < total; e += kSampThreads) {
-          int c = 0, j = e;
-          while (j >= s.ex.g_n[c]) j -= s.ex.g_n[c++];
-          const Cand me = s.ex.g[c][j];
-          int r = above;
-          u64 f = mass_above;
-          for (int c2 = 0; c2 < C; ++c2)
-            for (int q = 0; q < s.ex.g_n[c2]; ++q) {
-              const Cand& o = s.ex.g[c2][q];
-              if (o.z > me.z || (o.z == me.z && o.i < me.i)) { ++r; f += o.w; }
-            }
-          if (by_mass ? f < want && f + me.w >= want : r == k - 1) {
-            s.cut_z = me.z;
-            s.cut_i = me.i;
+      const int gn = lane < C ? s.ex.g_n[lane] : 0;
+      const int total = __reduce_add_sync(0xffffffffu, gn);
+      low = key_float(__reduce_min_sync(0xffffffffu, lane < C ? s.ex.g_min[lane] : 0xffffffffu));
+      hi = key_float(__reduce_max_sync(0xffffffffu, lane < C ? s.ex.g_max[lane] : 0u));
+      if (total <= kRank && __all_sync(0xffffffffu, gn <= gc)) {
+        // all candidates in one list; each is ranked by `span` neighbouring
+        // lanes; the cutoff is the last one kept
+        Cand* list = own_cand;
+        for (int e = tid; e < C * gc; e += kSampThreads) {
+          const int c = e / gc, j = e - c * gc;
+          if (j < s.ex.g_n[c]) {
+            int at = j;
+            for (int q = 0; q < c; ++q) at += s.ex.g_n[q];
+            list[at] = ex_cand[e];
           }
+        }
+        __syncthreads();
+        int span = 32;
+        while (span > 4 && span * total > kSampThreads) span /= 2;
+        const int e = tid / span;
+        const Cand me = list[min(e, total - 1)];
+        u64 f = 0;
+#pragma unroll 4
+        for (int q = tid % span; q < total; q += span) {
+          const Cand o = list[q];
+          f += o.z > me.z || (o.z == me.z && o.i < me.i) ? o.w : 0;
+        }
+        for (int o = span / 2; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+        f += mass_above;
+        if (e < total && f < want && f + me.w >= want) {
+          s.cut_z = me.z;
+          s.cut_i = me.i;
         }
         __syncthreads();
         cz = s.cut_z;
@@ -385,20 +461,20 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       }
       if (low == hi) {
         // equal logits: the r-th of them in index order
-        u64 r = by_mass ? (want - mass_above - 1) / fixed(low) + 1 : (u64)(k - above);
+        u64 r = by_mass ? (want - mass_above - 1) / fixed(low) + 1 : want - mass_above;
         r = min(r, (u64)total);
         int c = 0;
         while ((u64)s.ex.g_n[c] < r) r -= s.ex.g_n[c++];
         if (rank == c) {
           int n = 0;
-          for (int i = wbase; i < w * pw + pw; i += 32)
+          for (int i = i0; i < i1; i += 32)
             n += __popc(__ballot_sync(0xffffffffu, zs[i] == low && in_range(zs[i], i)));
           if (lane == 0) s.ired[w] = n;
           __syncthreads();
           int before = 0;
           for (int j = 0; j < w; ++j) before += s.ired[j];
           if ((int)r > before && (int)r <= before + n) {
-            for (int i = wbase; i < w * pw + pw; i += 32) {
+            for (int i = i0; i < i1; i += 32) {
               const bool t = zs[i] == low && in_range(zs[i], i);
               const unsigned bal = __ballot_sync(0xffffffffu, t);
               if (t && before + __popc(bal & ((2u << lane) - 1)) == (int)r)
@@ -421,51 +497,43 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   if (topp < 1.f) select(true);
 
   // ---- the draw ---------------------------------------------------------------
-  auto kept_weight = [&](int i) -> double {
-    const float v = zs[i];
-    return v > cz || (v == cz && base + i <= ci) ? weight(v) : 0.0;
+  // sum of the kept weights of n logits from i, `step` apart (n the same in
+  // all lanes)
+  auto kept_sum = [&](int i, int step, int n) -> double {
+    double sum = 0.0;
+    for (int q = 0; q < n; q += kU) {
+      float v[kU];
+      bool any = false;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int j = i + (q + u) * step;
+        v[u] = q + u < n ? zs[j] : -INFINITY;
+        if (!(v[u] > cz || (v[u] == cz && base + j <= ci))) v[u] = -INFINITY;
+        any |= v[u] > -INFINITY;
+      }
+      if (!__any_sync(0xffffffffu, any)) continue;
+      double x[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) x[u] = weight(v[u]);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) sum += x[u];
+    }
+    return sum;
   };
-  double sum = 0.0;
-#pragma unroll 4
-  for (int i = wbase; i < w * pw + pw; i += 32) sum += kept_weight(i);
+  const int run = pw / 32;
+  double sum = kept_sum(i0, 32, run);
   sum = wsum(sum);
   if (lane == 0) s.dred[w] = sum;
-  if (tid == 0) s.pick = -1;
   __syncthreads();
-  if (tid < C) {
-    double t = 0.0;
-#pragma unroll
-    for (int j = 0; j < kSW; ++j) t += s.dred[j];
-    put64(&s.ex.sum[rank], tid, __double_as_longlong(t));
+  if (w == 0) {
+    const double t = wsum(lane < kSW ? s.dred[lane] : 0.0);
+    if (lane < C) put64(&s.ex.sum[rank], lane, __double_as_longlong(t));
   }
   cluster_sync_all();
-  double total = 0.0;
-  for (int c = 0; c < C; ++c) total += s.ex.sum[c];
-  const double target = (uf > 0.f ? fmin((double)uf, 1.0) : 0.0) * total;
-  // the block and the warp whose share of the running mass holds the target;
-  // past the end (u = 1): the last with any mass
-  double run = 0.0, start = 0.0;
-  int at = -1;
-  for (int c = 0; c < C && (at < 0 || run <= target); ++c)
-    if (s.ex.sum[c] > 0.0) {
-      at = c;
-      start = run;
-      run += s.ex.sum[c];
-    }
-  if (rank != at) return;
-  run = start;
-  at = -1;
-  for (int j = 0; j < kSW && (at < 0 || run <= target); ++j)
-    if (s.dred[j] > 0.0) {
-      at = j;
-      start = run;
-      run += s.dred[j];
-    }
-  if (w != at) return;
-  run = start;
-  int token = -1, last = -1;
-  for (int i = wbase; i < w * pw + pw; i += 32) {
-    const double x = kept_weight(i);
+  // Which part of a sequence of shares holds the target: lane i has share x
+  // (0: none); *start: what lies before it.  Past the end (u = 1): the last
+  // with any mass.
+  auto holder = [&](double x, double from, double target, double* start) {
     double inc = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -473,21 +541,30 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       if (lane >= o) inc += y;
     }
     const unsigned any = __ballot_sync(0xffffffffu, x > 0.0);
-    const unsigned hit = __ballot_sync(0xffffffffu, x > 0.0 && run + inc > target);
-    if (any) last = i - lane + 31 - __clz(any);
-    if (hit) {
-      token = i - lane + __ffs(hit) - 1;
-      break;
-    }
-    run += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  if (token < 0) token = last;
+    const unsigned hit = __ballot_sync(0xffffffffu, x > 0.0 && from + inc > target);
+    const int at = hit ? __ffs(hit) - 1 : 31 - __clz(any);
+    const double before = __shfl_up_sync(0xffffffffu, inc, 1);
+    *start = from + __shfl_sync(0xffffffffu, lane == 0 ? 0.0 : before, at);
+    return at;
+  };
+  const double share = lane < C ? s.ex.sum[lane] : 0.0, total = wsum(share);
+  const double target = (uf > 0.f ? fmin((double)uf, 1.0) : 0.0) * total;
+  double start;
+  if (holder(share, 0.0, target, &start) != rank) return;
+  if (holder(lane < kSW ? s.dred[lane] : 0.0, start, target, &start) != w) return;
+  // this warp's logits, the lanes taking equal runs of them, then that lane's
+  // run, one logit per lane
+  double x = kept_sum(w * pw + lane * run, 1, run);
+  const int first = w * pw + run * holder(x, start, target, &start);
+  x = kept_sum(first + min(lane, run - 1), 1, 1);
+  if (lane >= run) x = 0.0;
+  const int token = first + holder(x, start, target, &start);
   if (lane == 0) {
     a.tokens[row] = base + token;
     if (a.logprobs) {
       const float v = zs[token];
-      const double x = v == m ? 0.0 : ((double)v - md) * inv_t;
-      a.logprobs[row] = (float)(x - log(total));
+      const double y = v == m ? 0.0 : ((double)v - md) * inv_t;
+      a.logprobs[row] = (float)(y - log(total));
     }
   }
 }
@@ -665,13 +742,12 @@ __global__ void __launch_bounds__(kAnyThreads) sample_any_kernel(SampleArgs a) {
   }
 }
 
-// Slices of up to 16384 logits: shared memory that every GPC can give a
-// 16-block cluster.
+// Slices of up to 16384 logits (the warps' histograms allow 1024 each), in
+// shared memory that every GPC can give a 16-block cluster.
 constexpr int kFit = 16384;
-constexpr size_t kMaxSmem = sizeof(Local) + kFit * 4;
 
-// Blocks per row: slices of up to 8192 logits, at most 16 blocks (8 where a
-// 16-block cluster, a non-portable size, cannot be scheduled).
+// Most blocks per row: 16, or 8 where a 16-block cluster (a non-portable
+// size) cannot be scheduled.
 int max_cluster() {
   constexpr int kMax = 64;
   static int n[kMax];
@@ -679,7 +755,8 @@ int max_cluster() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMax) return 8;
   if (n[dev]) return n[dev];
   auto k = sample_kernel;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) !=
+  const size_t smem = sample_smem(kMaxC, kFit);
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return 8;
   int c = 8, fit = 0;
@@ -687,7 +764,7 @@ int max_cluster() {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kMaxC, 1, 1);
     cfg.blockDim = dim3(kSampThreads);
-    cfg.dynamicSmemBytes = kMaxSmem;
+    cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kMaxC;
@@ -705,15 +782,18 @@ int max_cluster() {
 
 void launch_sample(const SampleArgs& a, cudaStream_t st) {
   const int most = max_cluster();
+  // few rows: small slices on as many SMs as there are; many: two blocks of
+  // full slices per SM, in clusters that are easier to place
+  const int slice = (int64_t)a.B * most <= 148 ? 8192 : kFit;
   int C = 1;
-  while (C < most && (int64_t)C * 8192 < a.V) C *= 2;
+  while (C < most && (int64_t)C * slice < a.V) C *= 2;
   if ((int64_t)C * kFit < a.V || (int64_t)C * a.B > 0x7fffffff) {
     launch_k(sample_any_kernel, dim3(a.B), dim3(kAnyThreads), 0, st, a);
     return;
   }
   const int pw = ((a.V + C * kSampThreads - 1) / (C * kSampThreads)) * 32;
   launch_k_cluster(sample_kernel, dim3(C * a.B), dim3(kSampThreads),
-                   sizeof(Local) + (size_t)kSW * pw * 4, st, C, a, C, pw);
+                   sample_smem(C, kSW * pw), st, C, a, C, pw);
 }
 
 }  // namespace dory
