@@ -55,24 +55,23 @@ __constant__ double kExpTab[16] = {
     0x1.6a09e667f3bcdp+0, 0x1.7a11473eb0187p+0, 0x1.8ace5422aa0dbp+0, 0x1.9c49182a3f090p+0,
     0x1.ae89f995ad3adp+0, 0x1.c199bdd85529cp+0, 0x1.d5818dcfba487p+0, 0x1.ea4afa2a490dap+0};
 
-// 2^(y/16) for y <= 0, relative error below 2^-41 + |y| 2^-53: y = 16 n + j + f,
-// |f| <= 1/2, by 2^n 2^(j/16) and the Taylor series of 2^(f/16) to f^5 (whose
-// next term is below 2^-42).  0 below y = -16000.  tab: 2^(j/16) in shared
-// memory (16 doubles, one per bank pair).  A weight off by 2^-41 moves a
-// border of the running sum by less than the chance 2^-32 of a uniform's
-// falling between.
+// 2^(y/16) for -1100 < y <= 0 (1 at 0), relative error below 2^-38: y = 16 n +
+// j + f, |f| <= 1/2, by 2^n 2^(j/16) and the polynomial of degree 4 through 1
+// at 0 whose largest relative error over |f| <= 1/2 is least (2.5e-12; fitted
+// by reweighted least squares).  tab: 2^(j/16) in shared memory (16 doubles,
+// one per bank pair).  An error of 2^-38 in the weights moves the borders of a
+// row's running sum so little that a uniform falls between with a chance
+// below 1e-6 at V = 131072, while sampling is bound by these f64 operations.
 __device__ __forceinline__ double exp2_16th(double y, const double* tab) {
-  constexpr double kMagic = 0x1.8p52, c = 0.693147180559945309417 / 16;
+  constexpr double kMagic = 0x1.8p52;
   const double t = y + kMagic, f = y - (t - kMagic);
   const int k = __double2loint(t);
-  double p = fma(f, c * c * c * c * c / 120, c * c * c * c / 24);
-  p = fma(p, f, c * c * c / 6);
-  p = fma(p, f, c * c / 2);
-  p = fma(p, f, c);
+  double p = fma(f, 0x1.3b29bf8ba0f3ap-23, 0x1.c6b3f5b3946b2p-17);
+  p = fma(p, f, 0x1.ebfbdfff31574p-11);
+  p = fma(p, f, 0x1.62e42fec3f16fp-5);
   p = fma(p, f, 1.0);
   p *= tab[k & 15];
-  const double v = __hiloint2double(__double2hiint(p) + ((k >> 4) << 20), __double2loint(p));
-  return y > -16000.0 ? v : 0.0;
+  return __hiloint2double(__double2hiint(p) + ((k >> 4) << 20), __double2loint(p));
 }
 
 template <typename T>
@@ -107,7 +106,8 @@ struct Cand {
 //                          stay below 2^32 (64-bit atomics on shared memory
 //                          ran 17 times slower); then the own candidates
 //   zs    f32 [per]        the slice
-//   bins  u8 [per]         bin of each logit in the last histogram
+//   bins  u32 [][threads]  bins of each thread's logits in the first histogram,
+//                          four to a word
 // A buffer that other blocks write is written again only after a barrier that
 // follows its last read.
 struct Fixed {
@@ -137,7 +137,7 @@ static_assert(sizeof(Fixed) % 16 == 0, "what follows is 16-byte aligned");
 __host__ __device__ inline int cand_cap(int C) { return C >= 4 ? 32 : kRank / C; }
 __host__ __device__ inline size_t sample_smem(int C, int per) {
   return sizeof(Fixed) + (size_t)C * kNB * 8 + (size_t)C * cand_cap(C) * sizeof(Cand) +
-         kHistWords * 4 + (size_t)per * 5;
+         kHistWords * 4 + (size_t)per * 4 + (size_t)(per / kSampThreads + 3) / 4 * kSampThreads * 4;
 }
 static_assert(kRank * sizeof(Cand) <= kHistWords * 4, "candidates fit the histograms' place");
 
@@ -153,8 +153,9 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   const int row = blockIdx.x / C, rank = blockIdx.x - row * C;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = kSW * pw, base = rank * per;      // this block's slice
-  const int i0 = w * pw + lane, i1 = w * pw + pw;   // this thread's part: i0, i0 + 32, ..
-  uint8_t* bins = reinterpret_cast<uint8_t*>(zs + per);
+  const int i0 = w * pw + lane, i1 = w * pw + pw;   // this thread's logits: i0, i0 + 32, ..
+  uint32_t* bins = reinterpret_cast<uint32_t*>(zs + per) + tid;
+  const int run = pw / 32;                          // logits per thread, at most 32
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if (tid < 16) s.tab[tid] = kExpTab[tid];
   pdl_wait();
@@ -169,26 +170,37 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   const float uf = a.uniform[row];
 
   // ---- the slice, its largest and smallest finite logit ---------------------
-  // (4-byte copies: rows need no alignment)
-#pragma unroll 4
-  for (int i = i0; i < i1; i += 32) {
-    if (base + i < a.V)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(su32(zs + i)), "l"(z + base + i)
-                   : "memory");
-    else
-      zs[i] = -INFINITY;
+  // (4-byte copies: rows need no alignment), in four parts, so that the first
+  // are looked at while the others arrive
+  const int part = (run + 3) / 4 * 32;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    for (int i = i0 + g * part; i < min(i1, i0 + (g + 1) * part); i += 32) {
+      if (base + i < a.V)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(su32(zs + i)),
+                     "l"(z + base + i)
+                     : "memory");
+      else
+        zs[i] = -INFINITY;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  uint32_t kmax = 0, kmin = 0xffffffffu;            // integer images
-#pragma unroll 4
-  for (int i = i0; i < i1; i += 32) {
-    const float v = clean(zs[i]);
-    zs[i] = v;
-    if (v > -INFINITY) {
-      kmax = max(kmax, key_of(v));
-      kmin = min(kmin, key_of(v));
+  float vmax = -INFINITY, vmin = INFINITY;          // of what may be drawn
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if (g == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    if (g == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    if (g == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if (g == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    for (int i = i0 + g * part; i < min(i1, i0 + (g + 1) * part); i += 32) {
+      const float v = zs[i];
+      vmax = fmaxf(vmax, v);                        // (passes over NaN)
+      vmin = v > -INFINITY ? fminf(vmin, v) : vmin;
     }
   }
+  // integer images (+ 0.f: -0 as +0)
+  uint32_t kmax = vmax > -INFINITY ? key_of(vmax + 0.f) : 0u;
+  uint32_t kmin = vmax > -INFINITY ? key_of(vmin + 0.f) : 0xffffffffu;
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   if (lane == 0) {
@@ -216,8 +228,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     }
     return;
   }
-  const float m = key_float(kmax);
-  float lo = m == INFINITY ? m : key_float(kmin);   // beside +inf nothing weighs anything
+  float m = key_float(kmax), lo = key_float(kmin);
   if (greedy) {
     // the lowest index of the largest logit, in the first block that has it
     const unsigned has = __ballot_sync(0xffffffffu, lane < C && s.ex.max[lane] == kmax);
@@ -235,13 +246,18 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     }
     return;
   }
+  if (m == INFINITY) {               // beside +inf nothing weighs anything
+    for (int i = i0; i < i1; i += 32) zs[i] = zs[i] == m ? 0.f : -INFINITY;
+    m = lo = 0.f;
+    kmax = key_of(m);
+  }
   const double inv_t = 1.0 / (double)T, md = (double)m;
   const double rate = inv_t * (16 / 0.693147180559945309417);
-  // (free of branches, so that kU of them overlap; -inf weighs 0)
-  auto weight = [&](float v) -> double {
-    const double x = exp2_16th(((double)v - md) * rate, s.tab);
-    return v == m ? 1.0 : x;
-  };
+  // Logits below `floor` weigh nothing: less than e^-44 of the largest, 2^-46
+  // of the mass for all of a row.
+  const float floor = m - 44.f * T;
+  // (free of branches, so that kU of them overlap; for v >= floor)
+  auto weight = [&](float v) -> double { return exp2_16th(((double)v - md) * rate, s.tab); };
   // weights as integers of 43 bits, nearest (adding 2^52 leaves them in the
   // low bits of the double)
   auto fixed = [&](float v) -> u64 {
@@ -251,13 +267,16 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   // kept: z > cz, or z == cz and index <= ci
   float cz = -INFINITY;
   int ci = -1;
+  bool cut = false;
   if (minp > 0.f) {
     // least logit with weight >= min_p: 32-way search of the integer images
     uint32_t l = key_of(lo), h = kmax;
     while (l < h) {
       const uint32_t step = (h - l) / 32 + 1;
       const uint32_t p = l + min(h - l, step * lane);
-      const unsigned ok = __ballot_sync(0xffffffffu, weight(key_float(p)) >= (double)minp);
+      const float v = key_float(p);
+      const unsigned ok = __ballot_sync(
+          0xffffffffu, v >= floor ? weight(fmaxf(v, floor)) >= (double)minp : false);
       const int f = ok ? __ffs(ok) - 1 : 32;          // lanes f.. hold
       if (f == 0) {
         h = l;
@@ -269,6 +288,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     }
     cz = key_float(h);
     ci = 0x7fffffff;
+    cut = true;
     lo = fmaxf(lo, cz);
   }
 
@@ -279,12 +299,15 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     if (by_mass) low = fmaxf(low, m - 31.f * T);
     low = fminf(low, hi);
     u64 mass_above = 0, want = 0;      // weights, or logits, before and up to the cutoff
+    uint32_t mask = 0;                 // this thread's logits still in question
     for (int level = 0;; ++level) {
       // histogram of the kept logits in [low, hi]
-      const bool flat = low == hi;
-      const double hd = (double)hi, sc = flat ? 0.0 : (double)kNB / (hd - (double)low);
-      auto in_range = [&](float v, int i) {
-        return v <= hi && v >= low && (v > cz || (v == cz && base + i <= ci));
+      const double hd = (double)hi, sc = low == hi ? 0.0 : (double)kNB / (hd - (double)low);
+      // bin of (hi - v) sc, rounded (monotone; the ends fall into the first and
+      // the last bin)
+      auto bin_of = [&](float v) {
+        const int q = __double2loint(fma(hd - (double)v, sc, 0x1.8p52 - 0.5));
+        return max(0, min(q, kNB - 1));
       };
       __syncthreads();
       for (int i = tid; i < kHistWords; i += kSampThreads) hist_all[i] = 0;
@@ -295,35 +318,46 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       }
       __syncthreads();
       uint32_t* hist = hist_all + w * 2 * kNB;
-      for (int ib = i0; ib < i1; ib += 32 * kU) {
-        float v[kU];
-        bool in[kU], any = false;
+      auto count = [&](int bn, u64 f) {
+        const uint32_t f0 = (uint32_t)f & 0x3fffffu, f1 = (uint32_t)(f >> 22);
+        if (f0) atomicAdd(hist + bn, f0);
+        if (f1) atomicAdd(hist + kNB + bn, f1);
+      };
+      if (level == 0) {
+        for (int q = 0; q < run; q += kU) {
+          float v[kU];
+          uint32_t in = 0;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int i = ib + 32 * u;
-          v[u] = i < i1 ? zs[i] : -INFINITY;
-          in[u] = v[u] > -INFINITY && in_range(v[u], i);
-          any |= in[u];
-        }
-        if (!__any_sync(0xffffffffu, any)) continue;
-        int bn[kU];
-        u64 f[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          // bin of (hi - v) sc, rounded (monotone; the ends fall into the
-          // first and the last bin)
-          const int q = __double2loint(fma(hd - (double)v[u], sc, 0x1.8p52 - 0.5));
-          bn[u] = flat ? 0 : max(0, min(q, kNB - 1));
-          f[u] = by_mass ? fixed(v[u]) : 1;
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-          if (in[u]) {
-            const uint32_t f0 = (uint32_t)f[u] & 0x3fffffu, f1 = (uint32_t)(f[u] >> 22);
-            bins[ib + 32 * u] = bn[u];
-            if (f0) atomicAdd(hist + bn[u], f0);
-            if (f1) atomicAdd(hist + kNB + bn[u], f1);
+          for (int u = 0; u < kU; ++u) {
+            const int i = i0 + 32 * (q + u);
+            v[u] = q + u < run ? zs[i] : -INFINITY;
+            bool ok = v[u] >= low;
+            if (cut) ok = ok && (v[u] > cz || (v[u] == cz && base + i <= ci));
+            in |= (uint32_t)ok << u;
           }
+          uint32_t word = 0xffffffffu;
+          if (__any_sync(0xffffffffu, in)) {
+            int bn[kU];
+            u64 f[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+              bn[u] = bin_of(v[u]);
+              f[u] = by_mass ? fixed(v[u]) : 1;
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+              if (in >> u & 1) {
+                word ^= (bn[u] ^ 255) << (8 * u);
+                count(bn[u], f[u]);
+              }
+          }
+          bins[(q / kU) * kSampThreads] = word;
+        }
+      } else {
+        for (uint32_t r = mask; r; r &= r - 1) {
+          const float v = zs[i0 + 32 * (__ffs(r) - 1)];
+          count(bin_of(v), by_mass ? fixed(v) : 1);
+        }
       }
       __syncthreads();
       if (tid < kNB) {
@@ -382,27 +416,49 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       mass_above = s.mass_above;
       want = s.want;
       // the bin's logits
-      uint32_t bmin = 0xffffffffu, bmax = 0;
-#pragma unroll 4
-      for (int i = i0; i < i1; i += 32) {
-        const float v = zs[i];
-        const bool hit = v > -INFINITY && in_range(v, i) && bins[i] == bin;
-        const unsigned bal = __ballot_sync(0xffffffffu, hit);
-        if (!bal) continue;
-        int at = 0;
-        if (lane == 0) at = atomicAdd(&s.n, __popc(bal));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(bal & ((1u << lane) - 1));
-        if (hit) {
-          if (at < gc) own_cand[at] = Cand{v, base + i, by_mass ? fixed(v) : 1};
-          bmin = min(bmin, key_of(v));
-          bmax = max(bmax, key_of(v));
+      if (level == 0) {
+        for (int q = 0; q < run; q += kU) {
+          const uint32_t e = __vcmpeq4(bins[(q / kU) * kSampThreads], bin * 0x01010101u) & 0x08040201u;
+          mask |= ((e | e >> 8 | e >> 16 | e >> 24) & 15u) << q;
+        }
+      } else {
+        for (uint32_t r = mask; r; r &= r - 1) {
+          const int q = __ffs(r) - 1;
+          if (bin_of(zs[i0 + 32 * q]) != bin) mask ^= 1u << q;
         }
       }
-      bmin = __reduce_min_sync(0xffffffffu, bmin);
-      bmax = __reduce_max_sync(0xffffffffu, bmax);
-      if (lane == 0 && bmax) {
-        atomicMin(&s.kmin, bmin);
-        atomicMax(&s.kmax, bmax);
+      float bmin = INFINITY, bmax = -INFINITY;
+      for (uint32_t r = mask; r; r &= r - 1) {
+        const float v = zs[i0 + 32 * (__ffs(r) - 1)];
+        bmin = fminf(bmin, v);
+        bmax = fmaxf(bmax, v);
+      }
+      const int mine = __popc(mask);
+      const int warps = __reduce_add_sync(0xffffffffu, mine);
+      int at = 0;
+      if (warps) {
+        const uint32_t k0 = __reduce_min_sync(0xffffffffu, mine ? key_of(bmin + 0.f) : 0xffffffffu);
+        const uint32_t k1 = __reduce_max_sync(0xffffffffu, mine ? key_of(bmax + 0.f) : 0u);
+        if (lane == 0) {
+          at = atomicAdd(&s.n, warps);
+          atomicMin(&s.kmin, k0);
+          atomicMax(&s.kmax, k1);
+        }
+        at = __shfl_sync(0xffffffffu, at, 0);
+      }
+      __syncthreads();
+      if (warps && s.n <= gc) {
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        at += inc - mine;
+        for (uint32_t r = mask; r; r &= r - 1, ++at) {
+          const int i = i0 + 32 * (__ffs(r) - 1);
+          own_cand[at] = Cand{zs[i], base + i, by_mass ? fixed(zs[i]) : 1};
+        }
       }
       __syncthreads();
       const int own = s.n;
@@ -411,7 +467,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
         put32(&s.ex.g_min[rank], tid, s.kmin);
         put32(&s.ex.g_max[rank], tid, s.kmax);
       }
-      const int send = min(own, gc);
+      const int send = own <= gc ? own : 0;
       for (int i = tid; i < C * send; i += kSampThreads) {
         const int c = i / send, j = i - c * send;
         const Cand x = own_cand[j];
@@ -466,19 +522,17 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
         int c = 0;
         while ((u64)s.ex.g_n[c] < r) r -= s.ex.g_n[c++];
         if (rank == c) {
-          int n = 0;
-          for (int i = i0; i < i1; i += 32)
-            n += __popc(__ballot_sync(0xffffffffu, zs[i] == low && in_range(zs[i], i)));
+          const int n = __reduce_add_sync(0xffffffffu, mine);
           if (lane == 0) s.ired[w] = n;
           __syncthreads();
           int before = 0;
           for (int j = 0; j < w; ++j) before += s.ired[j];
           if ((int)r > before && (int)r <= before + n) {
-            for (int i = i0; i < i1; i += 32) {
-              const bool t = zs[i] == low && in_range(zs[i], i);
+            for (int q = 0; q < run; ++q) {
+              const bool t = mask >> q & 1;
               const unsigned bal = __ballot_sync(0xffffffffu, t);
               if (t && before + __popc(bal & ((2u << lane) - 1)) == (int)r)
-                for (int q = 0; q < C; ++q) put32(&s.ex.tie, q, base + i);
+                for (int c2 = 0; c2 < C; ++c2) put32(&s.ex.tie, c2, base + i0 + 32 * q);
               before += __popc(bal);
             }
           }
@@ -492,36 +546,33 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   };
   if (k < a.V) {
     select(false);
+    cut = true;
     lo = fmaxf(lo, cz);
   }
   if (topp < 1.f) select(true);
 
   // ---- the draw ---------------------------------------------------------------
-  // sum of the kept weights of n logits from i, `step` apart (n the same in
-  // all lanes)
-  auto kept_sum = [&](int i, int step, int n) -> double {
-    double sum = 0.0;
-    for (int q = 0; q < n; q += kU) {
-      float v[kU];
-      bool any = false;
+  // weight of logit i of the slice, 0 if it is not kept
+  const float from = fmaxf(cz, floor);
+  auto kept = [&](float v, int i) { return v >= from && (v > cz || (v == cz && base + i <= ci)); };
+  double sum = 0.0;
+  for (int q = 0; q < run; q += kU) {
+    float v[kU];
+    bool in[kU], any = false;
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int j = i + (q + u) * step;
-        v[u] = q + u < n ? zs[j] : -INFINITY;
-        if (!(v[u] > cz || (v[u] == cz && base + j <= ci))) v[u] = -INFINITY;
-        any |= v[u] > -INFINITY;
-      }
-      if (!__any_sync(0xffffffffu, any)) continue;
-      double x[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) x[u] = weight(v[u]);
-#pragma unroll
-      for (int u = 0; u < kU; ++u) sum += x[u];
+    for (int u = 0; u < kU; ++u) {
+      const int i = i0 + 32 * (q + u);
+      v[u] = q + u < run ? zs[i] : -INFINITY;
+      in[u] = kept(v[u], i);
+      any |= in[u];
     }
-    return sum;
-  };
-  const int run = pw / 32;
-  double sum = kept_sum(i0, 32, run);
+    if (!__any_sync(0xffffffffu, any)) continue;
+    double x[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) x[u] = weight(in[u] ? v[u] : m);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) sum += in[u] ? x[u] : 0.0;
+  }
   sum = wsum(sum);
   if (lane == 0) s.dred[w] = sum;
   __syncthreads();
@@ -551,14 +602,27 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   const double target = (uf > 0.f ? fmin((double)uf, 1.0) : 0.0) * total;
   double start;
   if (holder(share, 0.0, target, &start) != rank) return;
+  // the warp whose part holds it; its logits, two neighbours per thread of the
+  // block
+  const int part_of = holder(lane < kSW ? s.dred[lane] : 0.0, start, target, &start);
+  double x[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int j = 2 * tid + u, i = part_of * pw + min(j, pw - 1);
+    const float v = zs[i];
+    const bool in = j < pw && kept(v, i);
+    const double y = weight(in ? v : m);
+    x[u] = in ? y : 0.0;
+  }
+  const double two = wsum(x[0] + x[1]);
+  __syncthreads();                                  // dred has been read
+  if (lane == 0) s.dred[w] = two;
+  __syncthreads();
   if (holder(lane < kSW ? s.dred[lane] : 0.0, start, target, &start) != w) return;
-  // this warp's logits, the lanes taking equal runs of them, then that lane's
-  // run, one logit per lane
-  double x = kept_sum(w * pw + lane * run, 1, run);
-  const int first = w * pw + run * holder(x, start, target, &start);
-  x = kept_sum(first + min(lane, run - 1), 1, 1);
-  if (lane >= run) x = 0.0;
-  const int token = first + holder(x, start, target, &start);
+  const int who = holder(x[0] + x[1], start, target, &start);
+  const double x0 = __shfl_sync(0xffffffffu, x[0], who), x1 = __shfl_sync(0xffffffffu, x[1], who);
+  const int token = part_of * pw + 2 * (32 * w + who) +
+                    (x0 == 0.0 || (x1 > 0.0 && !(start + x0 > target)));
   if (lane == 0) {
     a.tokens[row] = base + token;
     if (a.logprobs) {
