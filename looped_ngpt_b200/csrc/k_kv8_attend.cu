@@ -662,11 +662,11 @@ __global__ void kv8_merge_kernel(const Kv8AttendArgs a, int grid, int heads) {
 }
 
 // Thread blocks: one per SM (its stages fill the shared memory).
+constexpr int kMaxDevices = 64;
 int attend_grid() {
-  constexpr int kMax = 64;
-  static int n[kMax];
+  static int n[kMaxDevices];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMax) return 148;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
   if (!n[dev] &&
       cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 148;
@@ -678,8 +678,14 @@ void attend_t(const Kv8AttendArgs& a, const Kv8Maps& maps, cudaStream_t st) {
   using L = Att<HD>;
   const int grid = attend_grid();
   const size_t smem = L::smem(a.B);
-  cudaFuncSetAttribute(kv8_attend_kernel<HD, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)smem);
+  // once per device: shared memory for the largest batch
+  static bool set[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || !set[dev]) {
+    cudaFuncSetAttribute(kv8_attend_kernel<HD, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         (int)L::smem(kKv8MaxBatch));
+    if (dev >= 0 && dev < kMaxDevices) set[dev] = true;
+  }
   launch_k(kv8_attend_kernel<HD, G>, dim3(grid), dim3(32 * L::NW), smem, st, maps, a);
   // the fewer pairs, the more pieces each may have
   const int pairs = a.B * a.c.Hkv;

@@ -19,26 +19,28 @@ BLOCK = 32                # tokens per scale
 
 _I64x3 = ctypes.c_int64 * 3
 _I64x2 = ctypes.c_int64 * 2
+_F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
 
 
-def _need(t, name, dtype, shape, device):
+def _refuse(t, name, dtype, shape, device):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: {dtype} {shape} on {device} is needed, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} on {device} is "
+                     f"needed, got {t.dtype} {tuple(t.shape)}, strides "
+                     f"{t.stride()}, on {t.device}")
 
 
 def _dense(t, name, dtype, shape, device):
-    _need(t, name, dtype, shape, device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype
+            and t.shape == shape and t.device == device and t.is_contiguous()):
+        _refuse(t, name, dtype, shape, device)
     return t
 
 
-def _strided(t, name, n):
-    """Element strides of the first n dims; the last dim must be contiguous,
-    rows 16-byte aligned (the strides of dims of length 1 do not matter)."""
+def _rows(t, name, n):
+    """Element strides of the first n dims of a tensor whose last dim is
+    contiguous and whose rows are 16-byte aligned (the strides of dims of
+    length 1 do not matter)."""
     s = [0 if size == 1 else st for size, st in zip(t.shape[:n], t.stride())]
     if t.stride(-1) != 1 or t.data_ptr() % 16 or any(x % 8 for x in s):
         raise ValueError(f"{name}: the last dim must be contiguous and every "
@@ -60,19 +62,19 @@ class _On:
 
     def __init__(self, device, stream):
         if stream is None:
-            self.stream = torch.cuda.current_stream(device)
+            self.stream = torch._C._cuda_getCurrentRawStream(device.index)
             self.ctx = (None if torch.cuda.current_device() == device.index
                         else torch.cuda.device(device))
         else:
             if stream.device != device:
                 raise ValueError(f"stream: on {stream.device}, the tensors are "
                                  f"on {device}")
-            self.stream, self.ctx = stream, torch.cuda.stream(stream)
+            self.stream, self.ctx = stream.cuda_stream, torch.cuda.stream(stream)
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        return self.stream
 
     def __exit__(self, *exc):
         if self.ctx is not None:
@@ -89,35 +91,39 @@ def sample(logits, uniform, temperature=None, top_k=None, top_p=None,
     logprobs: True, or an f32 [B] tensor to write.  Returns (tokens, logprobs
     or None)."""
     dev = _cuda(logits, "logits")
-    if logits.dtype != torch.float32 or logits.dim() != 2:
+    if logits.dtype is not _F32 or logits.dim() != 2:
         raise ValueError("logits: float32 [B, V] is needed, got "
                          f"{logits.dtype} {tuple(logits.shape)}")
-    B, V = logits.shape
-    ld = logits.stride(0) if B > 1 else V
-    if V < 1 or (V > 1 and logits.stride(1) != 1) or ld < V:
+    B, V = row = logits.shape
+    ld, step = logits.stride()
+    if B <= 1:
+        ld = V
+    if V < 1 or (V > 1 and step != 1) or ld < V:
         raise ValueError("logits: rows must be contiguous and apart")
-    f32, i32, row = torch.float32, torch.int32, (B,)
-    _dense(uniform, "uniform", f32, row, dev)
-    for t, name, dt in ((temperature, "temperature", f32),
-                        (top_k, "top_k", i32), (top_p, "top_p", f32),
-                        (min_p, "min_p", f32), (tokens, "tokens", i32)):
-        if t is not None:
-            _dense(t, name, dt, row, dev)
+    row = row[:1]
+    _dense(uniform, "uniform", _F32, row, dev)
+    T = k = p = m = None
+    if temperature is not None:
+        T = _dense(temperature, "temperature", _F32, row, dev).data_ptr()
+    if top_k is not None:
+        k = _dense(top_k, "top_k", _I32, row, dev).data_ptr()
+    if top_p is not None:
+        p = _dense(top_p, "top_p", _F32, row, dev).data_ptr()
+    if min_p is not None:
+        m = _dense(min_p, "min_p", _F32, row, dev).data_ptr()
+    if tokens is not None:
+        _dense(tokens, "tokens", _I32, row, dev)
+    lp = None
+    if logprobs is not False and logprobs is not True:
+        lp = _dense(logprobs, "logprobs", _F32, row, dev)
     with _On(dev, stream) as st:
         if tokens is None:
-            tokens = torch.empty(row, dtype=i32, device=dev)
-        if isinstance(logprobs, torch.Tensor):
-            lp = _dense(logprobs, "logprobs", f32, row, dev)
-        else:
-            lp = torch.empty(row, dtype=f32, device=dev) if logprobs else None
+            tokens = torch.empty_like(uniform, dtype=_I32)
+        if logprobs is True:
+            lp = torch.empty_like(uniform)
         check("dory_sample", _lib.load().dory_sample(
-            logits.data_ptr(), ld, B, V,
-            None if temperature is None else temperature.data_ptr(),
-            None if top_k is None else top_k.data_ptr(),
-            None if top_p is None else top_p.data_ptr(),
-            None if min_p is None else min_p.data_ptr(),
-            uniform.data_ptr(), tokens.data_ptr(),
-            None if lp is None else lp.data_ptr(), st))
+            logits.data_ptr(), ld, B, V, T, k, p, m, uniform.data_ptr(),
+            tokens.data_ptr(), None if lp is None else lp.data_ptr(), st))
     return tokens, lp
 
 
@@ -157,6 +163,8 @@ class KV8Pages:
                          self.pages_per_seq, self.batch, shape[1], shape[3])
         self._ref = ctypes.byref(self.c)
         self._ws = {}
+        self._rows = self._q_rows = (None,)
+        self._q_heads = [g * shape[1] for g in (1, 2, 4, 8)]
 
     @classmethod
     def empty(cls, batch, max_ctx, n_kv_heads, head_dim, device="cuda"):
@@ -181,21 +189,28 @@ class KV8Pages:
             raise ValueError("k: bf16 [batch, T, n_kv_heads, head_dim] is needed")
         T = k.shape[1]
         shape = (B, T, self.n_kv_heads, self.head_dim)
-        _need(k, "k", torch.bfloat16, shape, dev)
-        _need(v, "v", torch.bfloat16, shape, dev)
+        for t, name in ((k, "k"), (v, "v")):
+            if not (isinstance(t, torch.Tensor) and t.dtype is _BF16
+                    and t.shape == shape and t.device == dev):
+                _refuse(t, name, _BF16, shape, dev)
         if T > self.pages_per_seq * PAGE:
             raise ValueError(f"{T} rows, a sequence holds "
                              f"{self.pages_per_seq * PAGE}")
-        _dense(pos, "pos", torch.int32, (B,), dev)
+        _dense(pos, "pos", _I32, (B,), dev)
         if n is not None:
-            _dense(n, "n", torch.int32, (B,), dev)
+            n = _dense(n, "n", _I32, (B,), dev).data_ptr()
         if T == 0:
             return
-        ks, vs = _I64x3(*_strided(k, "k", 3)), _I64x3(*_strided(v, "v", 3))
+        # the stride arrays of the last call, if the strides are the same
+        key = (T, k.stride(), v.stride())
+        pk, pv = k.data_ptr(), v.data_ptr()
+        if key != self._rows[0] or pk % 16 or pv % 16:
+            self._rows = (key, _I64x3(*_rows(k, "k", 3)),
+                          _I64x3(*_rows(v, "v", 3)))
+        _, ks, vs = self._rows
         with _On(dev, stream) as st:
             check("dory_kv8_append", _lib.load().dory_kv8_append(
-                self._ref, k.data_ptr(), v.data_ptr(), ks, vs, T,
-                pos.data_ptr(), None if n is None else n.data_ptr(), st))
+                self._ref, pk, pv, ks, vs, T, pos.data_ptr(), n, st))
 
     def workspace(self, n_q_heads):
         """A workspace for attend with n_q_heads query heads; one
@@ -219,26 +234,29 @@ class KV8Pages:
             raise ValueError("q: bf16 [batch, n_q_heads, head_dim] is needed")
         Hq = q.shape[1]
         shape = (B, Hq, hd)
-        _need(q, "q", torch.bfloat16, shape, dev)
-        if Hq not in [g * self.n_kv_heads for g in (1, 2, 4, 8)]:
+        if not (q.dtype is _BF16 and q.shape == shape and q.device == dev):
+            _refuse(q, "q", _BF16, shape, dev)
+        if Hq not in self._q_heads:
             raise ValueError(f"{Hq} query heads on {self.n_kv_heads} KV heads: "
                              "1, 2, 4 or 8 per KV head are needed")
-        _dense(lens, "lens", torch.int32, (B,), dev)
+        _dense(lens, "lens", _I32, (B,), dev)
         if window < 0:
             raise ValueError("window: 0 (off) or more is needed")
-        qs = _I64x2(*_strided(q, "q", 2))
+        key, pq = q.stride(), q.data_ptr()
+        if key != self._q_rows[0] or pq % 16:
+            self._q_rows = (key, _I64x2(*_rows(q, "q", 2)))
         if out is not None:
-            _dense(out, "out", torch.bfloat16, shape, dev)
+            _dense(out, "out", _BF16, shape, dev)
         with _On(dev, stream) as st:
             if out is None:
-                out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+                out = (torch.empty_like(q) if q.is_contiguous()
+                       else torch.empty(shape, dtype=_BF16, device=dev))
             if ws is None:
-                key = (st.value, Hq)
-                ws = self._ws.get(key)
+                ws = self._ws.get((st, Hq))
                 if ws is None:
-                    ws = self._ws[key] = self.workspace(Hq)
+                    ws = self._ws[st, Hq] = self.workspace(Hq)
             check("dory_kv8_attend", _lib.load().dory_kv8_attend(
-                self._ref, q.data_ptr(), qs, Hq, lens.data_ptr(), window,
+                self._ref, pq, self._q_rows[1], Hq, lens.data_ptr(), window,
                 hd ** -0.5 if scale is None else scale, out.data_ptr(),
                 ws.data_ptr(), ws.numel(), st))
         return out
