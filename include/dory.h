@@ -52,6 +52,7 @@ extern "C" {
 #define DORY_ERR_DEVICE (-7)      /* a device-side check recorded an error   */
 
 typedef enum { DORY_KV_PER_LOOP = 0, DORY_KV_LAST_LOOP = 1 } dory_kv_mode;
+typedef enum { DORY_KV_BF16 = 0, DORY_KV_E4M3 = 1 } dory_kv_fmt;
 typedef enum { DORY_W_BF16 = 0, DORY_W_MXFP8 = 1, DORY_W_NVFP4 = 2 } dory_wfmt;
 
 /* Model shape.  A block is an attention sublayer followed by an MLP
@@ -142,6 +143,34 @@ int dory_kv_cache_bytes(const dory_model* m, int batch, int max_ctx,
 int dory_kv_cache_bind(dory_model* m, void* d_buf, int64_t bytes, int batch,
                        int max_ctx, int max_chunk, int max_loops, int kv_mode,
                        void* stream, dory_cache** out);
+
+/* The same two calls with a storage format for the full-attention layers'
+ * K/V entries (whose pages make up nearly all of a long context's cache;
+ * dory_kv_cache_bytes / _bind are the DORY_KV_BF16 case).  DORY_KV_E4M3
+ * holds them in 8 bits as dory_kv8 does, one power-of-two scale per 32 tokens
+ * and KV head; sliding-window layers keep their bf16 rings.
+ *   - Every call writes its tokens' K/V as dory_kv8_append does (from the
+ *     bf16 values a bf16 cache would hold), then its queries read the cached
+ *     values, their own tokens' among them.  One-token calls read the 8-bit
+ *     pages (dory_kv8_attend); multi-token calls decode a layer to one bf16
+ *     layer kept behind the pages (present when max_chunk > 1, so the buffer
+ *     is half of a bf16 cache's pages plus one bf16 layer).
+ *   - A scale never shrinks while its block holds older tokens, so cutting a
+ *     prompt differently can change an entry by one subnormal step.
+ *   - dory_cache_copy_prefix needs the same format on both sides and copies
+ *     codes and scales as they are; dory_cache_fill_synthetic stores its
+ *     bf16 values as one append does; dory_spec_decode_step refuses these
+ *     caches (DORY_ERR_UNSUPPORTED): a rejected draft could have grown a
+ *     scale.
+ * Errors as above, and DORY_ERR_UNSUPPORTED for more than 2048 sequences or
+ * 2^31 cached rows x KV heads in DORY_KV_E4M3. */
+int dory_kv_cache_bytes_fmt(const dory_model* m, int batch, int max_ctx,
+                            int max_chunk, int max_loops, int kv_mode,
+                            int kv_fmt, int64_t* bytes);
+int dory_kv_cache_bind_fmt(dory_model* m, void* d_buf, int64_t bytes, int batch,
+                           int max_ctx, int max_chunk, int max_loops,
+                           int kv_mode, int kv_fmt, void* stream,
+                           dory_cache** out);
 
 /* Tokens currently held per sequence (host mirror; all sequences of a cache
  * advance together). */

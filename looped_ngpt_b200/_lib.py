@@ -16,6 +16,7 @@ ERRORS = {-1: "DORY_ERR_ARG", -2: "DORY_ERR_UNSUPPORTED", -3: "DORY_ERR_CACHE",
           -4: "DORY_ERR_CUDA", -5: "DORY_ERR_TIMEOUT", -6: "DORY_ERR_WORKSPACE",
           -7: "DORY_ERR_DEVICE"}
 KV_MODES = {"per_loop": 0, "last_loop": 1}
+KV_FMTS = {"bf16": 0, "e4m3": 1}
 
 
 class DoryConfig(Structure):
@@ -53,6 +54,11 @@ SIGNATURES = {
                                     _I64P]),
     "dory_kv_cache_bind": (c_int, [_P, _P, c_int64, c_int, c_int, c_int, c_int,
                                    c_int, _P, POINTER(c_void_p)]),
+    "dory_kv_cache_bytes_fmt": (c_int, [_P, c_int, c_int, c_int, c_int, c_int,
+                                        c_int, _I64P]),
+    "dory_kv_cache_bind_fmt": (c_int, [_P, _P, c_int64, c_int, c_int, c_int,
+                                       c_int, c_int, c_int, _P,
+                                       POINTER(c_void_p)]),
     "dory_cache_length": (c_int, [_P, POINTER(c_int)]),
     "dory_cache_reset": (c_int, [_P, _P]),
     "dory_cache_fill_synthetic": (c_int, [_P, _P, c_int, ctypes.c_uint64, _P]),

@@ -120,7 +120,7 @@ struct dory_model {
 
 struct dory_cache {
   dory_model* m;
-  int B, max_ctx, max_chunk, max_loops, kv_mode;
+  int B, max_ctx, max_chunk, max_loops, kv_mode, kv_fmt;
   int n_ctx = 0;
   int loops_bound = 0;
   int pages_per_seq;
@@ -131,6 +131,13 @@ struct dory_cache {
   std::vector<KVSlot> slots;
   std::vector<CUtensorMap> kv_maps;   // per slot: decode maps of K, then V
   std::vector<CUtensorMap> pf_maps;   // per slot: prefill maps K64, K32, V64, V32
+  // kv_fmt E4M3: per slot (unset for sliding-window layers, whose rings stay
+  // bf16).  `slots` holds the one bf16 layer that multi-token calls decode a
+  // layer into; d_lens [B] and ws belong to the one-token calls' attention.
+  std::vector<Kv8> kv8;
+  std::vector<Kv8Maps> kv8_maps;
+  int* d_lens = nullptr;
+  void* d_attn_ws = nullptr;
 };
 
 namespace {
@@ -147,14 +154,15 @@ int slots_of(const dory_model* m, int i, int kv_mode, int max_loops) {
 
 struct CacheLayout {
   size_t header, table, total;
-  std::vector<size_t> k_off, v_off;
+  std::vector<size_t> k_off, v_off, ks_off, vs_off;   // scales: kv_fmt E4M3
+  size_t lens, attn_ws;
   std::vector<int> ring, cap;
   std::vector<int> base;
   int pages_per_seq, swa_cap;
 };
 
 CacheLayout cache_layout(const dory_model* m, int B, int max_ctx,
-                         int max_chunk, int max_loops, int kv_mode) {
+                         int max_chunk, int max_loops, int kv_mode, int kv_fmt) {
   CacheLayout L;
   const Dims& dm = m->dm;
   L.pages_per_seq = (max_ctx + kPage - 1) / kPage;
@@ -169,17 +177,35 @@ CacheLayout cache_layout(const dory_model* m, int B, int max_ctx,
     L.base.push_back((int)L.k_off.size());
     const int n = slots_of(m, i, kv_mode, max_loops);
     for (int s = 0; s < n; ++s) {
-      const bool full = m->ltype[i] == 1;
+      const bool full = m->ltype[i] == 1, e4m3 = full && kv_fmt == DORY_KV_E4M3;
       const size_t per =
-          full ? (size_t)B * L.pages_per_seq * dm.Hkv * kPage * dm.hd * 2
+          full ? (size_t)B * L.pages_per_seq * dm.Hkv * kPage * dm.hd * (e4m3 ? 1 : 2)
                : (size_t)B * dm.Hkv * L.swa_cap * dm.hd * 2;
+      const size_t scales = e4m3 ? (size_t)B * L.pages_per_seq * dm.Hkv * 2 * 4 : 0;
       L.k_off.push_back(off);
       off += align256(per);
       L.v_off.push_back(off);
       off += align256(per);
+      L.ks_off.push_back(off);
+      off += align256(scales);
+      L.vs_off.push_back(off);
+      off += align256(scales);
       L.ring.push_back(full ? 0 : 1);
       L.cap.push_back(full ? 0 : L.swa_cap);
     }
+  }
+  if (kv_fmt == DORY_KV_E4M3) {
+    // after the slots: the bf16 layer of multi-token calls (one more slot)
+    const size_t per = max_chunk > 1
+                           ? (size_t)B * L.pages_per_seq * dm.Hkv * kPage * dm.hd * 2 : 0;
+    L.k_off.push_back(off);
+    off += align256(per);
+    L.v_off.push_back(off);
+    off += align256(per);
+    L.lens = off;
+    off += align256((size_t)B * sizeof(int));
+    L.attn_ws = off;
+    off += align256(kv8_attend_ws(dm.Hq / dm.Hkv, dm.hd));
   }
   L.total = off;
   return L;
@@ -422,31 +448,52 @@ void dory_free(dory_model* m) {
   delete m;
 }
 
-int dory_kv_cache_bytes(const dory_model* m, int batch, int max_ctx,
-                        int max_chunk, int max_loops, int kv_mode,
-                        int64_t* bytes) {
+int dory_kv_cache_bytes_fmt(const dory_model* m, int batch, int max_ctx,
+                            int max_chunk, int max_loops, int kv_mode,
+                            int kv_fmt, int64_t* bytes) {
   if (!m || !bytes || batch < 1 || max_ctx < 1 || max_chunk < 1 ||
-      max_chunk > max_ctx || (kv_mode != 0 && kv_mode != 1))
+      max_chunk > max_ctx || (kv_mode != 0 && kv_mode != 1) ||
+      (kv_fmt != DORY_KV_BF16 && kv_fmt != DORY_KV_E4M3))
     return DORY_ERR_ARG;
   if (kv_mode == DORY_KV_PER_LOOP && max_loops < 1) return DORY_ERR_ARG;
   if (kv_mode == DORY_KV_LAST_LOOP) max_loops = 1;
+  if (kv_fmt == DORY_KV_E4M3) {
+    // the limits of the 8-bit attention (32-bit block counts and TMA rows)
+    const int64_t pages = (int64_t)batch * ((max_ctx + (int64_t)kPage - 1) / kPage);
+    if (batch > kKv8MaxBatch || pages * m->dm.Hkv * kPage > 0x7fffffff)
+      return DORY_ERR_UNSUPPORTED;
+  }
   *bytes = (int64_t)cache_layout(m, batch, max_ctx, max_chunk, max_loops,
-                                 kv_mode).total;
+                                 kv_mode, kv_fmt).total;
   return DORY_OK;
+}
+
+int dory_kv_cache_bytes(const dory_model* m, int batch, int max_ctx,
+                        int max_chunk, int max_loops, int kv_mode,
+                        int64_t* bytes) {
+  return dory_kv_cache_bytes_fmt(m, batch, max_ctx, max_chunk, max_loops, kv_mode,
+                                 DORY_KV_BF16, bytes);
 }
 
 int dory_kv_cache_bind(dory_model* m, void* d_buf, int64_t bytes, int batch,
                        int max_ctx, int max_chunk, int max_loops, int kv_mode,
                        void* stream, dory_cache** out) {
+  return dory_kv_cache_bind_fmt(m, d_buf, bytes, batch, max_ctx, max_chunk, max_loops,
+                                kv_mode, DORY_KV_BF16, stream, out);
+}
+
+int dory_kv_cache_bind_fmt(dory_model* m, void* d_buf, int64_t bytes, int batch,
+                           int max_ctx, int max_chunk, int max_loops, int kv_mode,
+                           int kv_fmt, void* stream, dory_cache** out) {
   if (!out) return DORY_ERR_ARG;
   *out = nullptr;
   int64_t need = 0;
-  int rc = dory_kv_cache_bytes(m, batch, max_ctx, max_chunk, max_loops,
-                               kv_mode, &need);
+  int rc = dory_kv_cache_bytes_fmt(m, batch, max_ctx, max_chunk, max_loops,
+                                   kv_mode, kv_fmt, &need);
   if (rc) return rc;
   if (!d_buf || ((uintptr_t)d_buf & 255) || bytes < need) return DORY_ERR_ARG;
   if (kv_mode == DORY_KV_LAST_LOOP) max_loops = 1;
-  CacheLayout L = cache_layout(m, batch, max_ctx, max_chunk, max_loops, kv_mode);
+  CacheLayout L = cache_layout(m, batch, max_ctx, max_chunk, max_loops, kv_mode, kv_fmt);
   dory_cache* c = new dory_cache();
   c->m = m;
   c->B = batch;
@@ -454,37 +501,55 @@ int dory_kv_cache_bind(dory_model* m, void* d_buf, int64_t bytes, int batch,
   c->max_chunk = max_chunk;
   c->max_loops = max_loops;
   c->kv_mode = kv_mode;
+  c->kv_fmt = kv_fmt;
   c->pages_per_seq = L.pages_per_seq;
   c->swa_cap = L.swa_cap;
   char* base = (char*)d_buf;
   c->d_nctx = (int*)base;
   c->d_block_table = (int*)(base + L.header);
   c->slot_base = L.base;
-  for (size_t i = 0; i < L.k_off.size(); ++i) {
-    const KVSlot kv{(bf16*)(base + L.k_off[i]), (bf16*)(base + L.v_off[i]),
+  const int hd = m->dm.hd, tk = pf_tile_keys();
+  const int n_pages = batch * L.pages_per_seq;
+  const size_t n_slots = L.ring.size();
+  for (size_t i = 0; i < n_slots; ++i) {
+    const bool e4m3 = kv_fmt == DORY_KV_E4M3 && !L.ring[i];
+    const size_t at = e4m3 ? n_slots : i;       // the bf16 rows of this slot
+    const KVSlot kv{(bf16*)(base + L.k_off[at]), (bf16*)(base + L.v_off[at]),
                     L.ring[i], L.cap[i]};
     c->slots.push_back(kv);
     // rows of the [rows][hd] view: ring slots, or every page's rows
     const long rows = kv.ring ? (long)batch * m->dm.Hkv * kv.cap
-                              : (long)batch * L.pages_per_seq * m->dm.Hkv * kPage;
-    CUtensorMap mk, mv;
-    if (!make_kv_tile_map(&mk, kv.K, rows, m->dm.hd) ||
-        !make_kv_tile_map(&mv, kv.V, rows, m->dm.hd)) {
+                              : (long)n_pages * m->dm.Hkv * kPage;
+    CUtensorMap mk{}, mv{}, pm[4] = {};
+    Kv8 q{};
+    Kv8Maps qm{};
+    bool ok = true;
+    if (e4m3) {
+      q = Kv8{(uint8_t*)(base + L.k_off[i]), (uint8_t*)(base + L.v_off[i]),
+              (float*)(base + L.ks_off[i]), (float*)(base + L.vs_off[i]),
+              c->d_block_table, n_pages, L.pages_per_seq, m->dm.Hkv, hd};
+      ok = make_kv8_maps(q, &qm);
+    } else {
+      ok = make_kv_tile_map(&mk, kv.K, rows, hd) && make_kv_tile_map(&mv, kv.V, rows, hd);
+    }
+    if (!e4m3 || max_chunk > 1)
+      ok = ok && make_map_2d(&pm[0], kv.K, rows, hd, hd, 64, tk) &&
+           make_map_2d(&pm[1], kv.K, rows, hd, hd, 32, tk) &&
+           make_map_2d(&pm[2], kv.V, rows, hd, hd, 64, tk) &&
+           make_map_2d(&pm[3], kv.V, rows, hd, hd, 32, tk);
+    if (!ok) {
       delete c;
       return DORY_ERR_CUDA;
     }
     c->kv_maps.push_back(mk);
     c->kv_maps.push_back(mv);
-    CUtensorMap pm[4];
-    const int hd = m->dm.hd, tk = pf_tile_keys();
-    if (!make_map_2d(&pm[0], kv.K, rows, hd, hd, 64, tk) ||
-        !make_map_2d(&pm[1], kv.K, rows, hd, hd, 32, tk) ||
-        !make_map_2d(&pm[2], kv.V, rows, hd, hd, 64, tk) ||
-        !make_map_2d(&pm[3], kv.V, rows, hd, hd, 32, tk)) {
-      delete c;
-      return DORY_ERR_CUDA;
-    }
     for (int k = 0; k < 4; ++k) c->pf_maps.push_back(pm[k]);
+    c->kv8.push_back(q);
+    c->kv8_maps.push_back(qm);
+  }
+  if (kv_fmt == DORY_KV_E4M3) {
+    c->d_lens = (int*)(base + L.lens);
+    c->d_attn_ws = base + L.attn_ws;
   }
   // finite contents everywhere: attention tiles also cover rows that no
   // token has written yet (their probabilities are 0, their values must not
@@ -744,6 +809,8 @@ void enqueue_forward(const CallCtx& x) {
     if (i == m->n_in) rj = (t == 1) ? RJ_FIRST : RJ_NEXT;
     const bool full = m->ltype[i] == 1;
     const KVSlot kv = slot_for(x.c, i, t);
+    const int slot = slot_index(x.c, i, t);
+    const bool kv8 = full && x.c->kv_fmt == DORY_KV_E4M3;
 
     // ---- attention sublayer -------------------------------------------
     int S_qkvg = 1;
@@ -802,13 +869,43 @@ void enqueue_forward(const CallCtx& x) {
       da.row_loops = x.row_loops; da.loop_t = t;
       const double nk = full ? x.n_ctx0 + 1.0
                              : std::min(x.n_ctx0 + 1.0, (double)dm.window);
-      if (gemv && x.B * dm.Hkv * nk * dm.hd * 4.0 < kL2pfMaxKvBytes)
-        set_l2_prefetch(m, bw, da.l2pf);
-      Prof p(m, x.st, "attn_decode",
-             x.B * (dm.Hkv * nk * dm.hd * 4.0 + S_qkvg * dm.rows_qkvg * 4.0),
-             4.0 * x.B * dm.Hq * nk * dm.hd);
-      launch_attn_decode(da, &x.c->kv_maps[2 * slot_index(x.c, i, t)], x.st);
+      if (kv8) {
+        da.q_scale = 1.f;
+        const Kv8& c8 = x.c->kv8[slot];
+        {
+          Prof p(m, x.st, "kv8_form", (double)x.B * S_qkvg * dm.rows_qkvg * 4.0, 0);
+          launch_kv8_form(Kv8FormArgs{da, c8, w.qb, w.gate, x.c->d_lens}, x.st);
+        }
+        Kv8AttendArgs ka{};
+        ka.c = c8; ka.B = x.B; ka.G = dm.Hq / dm.Hkv;
+        ka.q = w.qb; ka.qs_b = dm.qdim; ka.qs_h = dm.hd;
+        ka.len = x.c->d_lens; ka.scale = sqrtf((float)dm.hd);
+        ka.out = w.a; ka.ws = x.c->d_attn_ws; ka.err = m->d_status; ka.gate = w.gate;
+        Prof p(m, x.st, "attn_kv8", x.B * (dm.Hkv * nk * dm.hd * 2.0 + dm.qdim * 8.0),
+               4.0 * x.B * dm.Hq * nk * dm.hd);
+        launch_kv8_attend(ka, x.c->kv8_maps[slot], x.st);
+      } else {
+        if (gemv && x.B * dm.Hkv * nk * dm.hd * 4.0 < kL2pfMaxKvBytes)
+          set_l2_prefetch(m, bw, da.l2pf);
+        Prof p(m, x.st, "attn_decode",
+               x.B * (dm.Hkv * nk * dm.hd * 4.0 + S_qkvg * dm.rows_qkvg * 4.0),
+               4.0 * x.B * dm.Hq * nk * dm.hd);
+        launch_attn_decode(da, &x.c->kv_maps[2 * slot], x.st);
+      }
     } else {
+      if (kv8) {
+        // the chunk's rows, which the projection left in the cache's bf16
+        // layer, become codes; then every query reads the cached values
+        const Kv8& c8 = x.c->kv8[slot];
+        {
+          Prof p(m, x.st, "kv8_append", (double)x.M * dm.kvdim * 6.0, 0);
+          launch_kv8_append(Kv8AppendArgs{c8, x.B, x.T, kv.K, kv.V, 0, 0, 0, 0, 0, 0, nullptr,
+                                          nullptr, m->d_status, geo.n_ctx, x.row_loops, t},
+                            x.st);
+        }
+        Prof p(m, x.st, "kv8_decode", (double)x.B * (x.n_ctx0 + x.T) * dm.kvdim * 6.0, 0);
+        launch_kv8_decode(c8, x.B, geo.n_ctx, x.T, kv.K, kv.V, x.st);
+      }
       AttnArgs aa{};
       aa.q = w.qb; aa.gate = w.gate; aa.B = x.B; aa.T = x.T; aa.dm = dm;
       aa.window = full ? 0 : dm.window; aa.kv = kv; aa.g = geo;
@@ -823,7 +920,7 @@ void enqueue_forward(const CallCtx& x) {
       Prof p(m, x.st, "attn_prefill",
              x.B * (dm.Hkv * keys * dm.hd * 4.0) + x.M * dm.qdim * 10.0,
              4.0 * x.B * dm.Hq * vis * dm.hd);
-      launch_attn_prefill_tc(aa, &x.c->pf_maps[4 * slot_index(x.c, i, t)], x.st);
+      launch_attn_prefill_tc(aa, &x.c->pf_maps[4 * slot], x.st);
     }
     int S_o = 1;
     if (gemv) {
@@ -1105,7 +1202,7 @@ int dory_spec_decode_step(dory_model* m, dory_cache* c, const int32_t* d_last,
       (temperature > 0.f && !d_uniform) || ((uintptr_t)d_workspace & 255))
     return DORY_ERR_ARG;
   *n_out = 0;
-  if (m->wfmt != DORY_W_BF16) return DORY_ERR_UNSUPPORTED;
+  if (m->wfmt != DORY_W_BF16 || c->kv_fmt != DORY_KV_BF16) return DORY_ERR_UNSUPPORTED;
   if (gamma + 1 > c->max_chunk) return DORY_ERR_ARG;
   const int n0 = c->n_ctx;
   if ((int64_t)n0 + gamma + 1 > c->max_ctx) return DORY_ERR_CACHE;
@@ -1372,6 +1469,10 @@ extern "C" int dory_cache_fill_synthetic(dory_model* m, dory_cache* c,
       const int gslot = (ns > 1 || (is_rec(m, i) &&
                                      c->kv_mode == DORY_KV_PER_LOOP))
                             ? s2 + 1 : 0;
+      if (!kv.ring && c->kv_fmt == DORY_KV_E4M3) {
+        launch_kv8_fill(c->kv8[c->slot_base[i] + s2], c->B, n_ctx, i, gslot, seed, ck, cv, st);
+        continue;
+      }
       const int lo = kv.ring ? std::max(0, n_ctx - kv.cap) : 0;
       launch_fill_kv(kv, geo, c->B, dm.Hkv, dm.hd, lo, n_ctx, i, gslot, seed,
                      ck, cv, st);
@@ -1455,7 +1556,7 @@ extern "C" int dory_cache_copy_prefix(dory_model* m, dory_cache* dst,
   if (!m || !dst || !src || dst == src || dst->m != m || src->m != m ||
       src_b < 0 || src_b >= src->B || n_tokens < 0)
     return DORY_ERR_ARG;
-  if (dst->kv_mode != src->kv_mode || n_tokens > src->n_ctx ||
+  if (dst->kv_mode != src->kv_mode || dst->kv_fmt != src->kv_fmt || n_tokens > src->n_ctx ||
       n_tokens > dst->max_ctx)
     return DORY_ERR_CACHE;
   // the loops the source's per_loop slots hold
@@ -1482,6 +1583,11 @@ extern "C" int dory_cache_copy_prefix(dory_model* m, dory_cache* dst,
     for (int t = 0; t < ns; ++t) {
       const KVSlot& a = src->slots[src->slot_base[i] + t];
       const KVSlot& b = dst->slots[dst->slot_base[i] + t];
+      if (!a.ring && src->kv_fmt == DORY_KV_E4M3) {
+        launch_kv8_copy_prefix(src->kv8[src->slot_base[i] + t], src_b,
+                               dst->kv8[dst->slot_base[i] + t], dst->B, n_tokens, st);
+        continue;
+      }
       const int lo = a.ring ? sw_lo : 0;
       launch_copy_prefix(a, gs, src_b, b, gd, dst->B, dm.Hkv, dm.hd, lo,
                          n_tokens, st);

@@ -214,6 +214,28 @@ void launch_set_nctx(int* n_ctx, int v, cudaStream_t st);
 void launch_fill_kv(const KVSlot& kv, const CacheGeo& g, int B, int Hkv,
                     int hd, int p_lo, int p_hi, int block, int slot,
                     uint64_t seed, float ck, float cv, cudaStream_t st);
+// SplitMix64 output function (Steele, Lea and Flood, 2014).
+__device__ __forceinline__ uint64_t splitmix64(uint64_t x) {
+  uint64_t z = x + 0x9E3779B97F4A7C15ull;
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  return z ^ (z >> 31);
+}
+// Synthetic entry (kind, block, slot, b, kvh, pos, j): the SplitMix64 counter
+// generator's uniform u scaled to (2u - 1) * c.
+__device__ __forceinline__ float synthetic_kv(int kind, int block, int slot, int b,
+                                              int kvh, int pos, int j, uint64_t seed,
+                                              float c) {
+  uint64_t n = (uint64_t)kind;
+  n = n * 64 + (uint64_t)block;
+  n = n * 8 + (uint64_t)slot;
+  n = n * 4096 + (uint64_t)b;
+  n = n * 64 + (uint64_t)kvh;
+  n = n * (1ull << 20) + (uint64_t)pos;
+  n = n * 512 + (uint64_t)j;
+  const float u = __fmul_rn((float)(splitmix64(seed + n) >> 40), 0x1p-24f);
+  return __fmul_rn(__fsub_rn(__fmul_rn(2.f, u), 1.f), c);
+}
 void launch_cache_init(int* n_ctx, int* block_table, int B, int pages_per_seq,
                        cudaStream_t st);
 // K/V entries of positions [p_lo, p_hi) of sequence src_b of one layer slot
@@ -381,6 +403,12 @@ struct Kv8AppendArgs {
   const int* pos;                           // [B] tokens held before
   const int* n;                             // [B] rows to append, or null (T)
   int* err;
+  // pos == null: k and v are pages like the codes' (bf16 [n_pages][Hkv][kPage]
+  // [hd]), rows of positions n_ctx .. n_ctx + T - 1 of every sequence that
+  // takes part in loop loop_t (row_writes_kv)
+  const int* n_ctx;
+  const int* row_loops;
+  int loop_t;
 };
 void launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st);
 
@@ -395,6 +423,7 @@ struct Kv8AttendArgs {
   bf16* out;                                // [B][Hkv * G][hd]
   void* ws;
   int* err;
+  const float* gate;                        // [B][Hkv * G][hd] factors, or null
 };
 // TMA maps of a cache's codes: the first 64 or 128 bytes of a row of K and
 // of V, then (head_dim 160) the last 32.
@@ -406,6 +435,30 @@ void launch_kv8_attend(const Kv8AttendArgs& a, const Kv8Maps& maps,
                        cudaStream_t st);
 constexpr int kKv8MaxBatch = 2048;  // the attention's block prefix in shared memory
 size_t kv8_attend_ws(int G, int hd);
+
+// One-token calls of a model: q (bf16, unscaled), the gate's sigmoid and the
+// key count (n_ctx + 1) of every sequence from the QKVG partials; the new K/V
+// row goes into the cache as kv8_append would put it there.
+struct Kv8FormArgs {
+  DecAttnArgs d;           // qkvg, S, B, dm, s_q, s_k, rope, q_scale, g, row loops
+  Kv8 c;
+  bf16* q;                 // [B][qdim]
+  float* gate;             // [B][qdim]
+  int* lens;               // [B]
+};
+void launch_kv8_form(const Kv8FormArgs& a, cudaStream_t st);
+// The values of positions 0 .. n_ctx + T - 1 of every sequence, bf16 (exact:
+// 4 significant bits times a power of two), in pages like the codes'.
+void launch_kv8_decode(const Kv8& c, int B, const int* n_ctx, int T, bf16* k,
+                       bf16* v, cudaStream_t st);
+// Seeded synthetic entries of positions 0 .. n - 1 (launch_fill_kv), appended
+// to an empty cache.
+void launch_kv8_fill(const Kv8& c, int B, int n, int block, int slot,
+                     uint64_t seed, float ck, float cv, cudaStream_t st);
+// Positions 0 .. n - 1 of sequence src_b to every sequence of dst, codes and
+// scales as they are.
+void launch_kv8_copy_prefix(const Kv8& src, int src_b, const Kv8& dst, int B_dst,
+                            int n, cudaStream_t st);
 
 // Device status word of the current device (null if it cannot be found).
 int* device_status_word();

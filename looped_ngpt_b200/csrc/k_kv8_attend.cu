@@ -91,6 +91,16 @@ __device__ __forceinline__ uint32_t tile_off(int r, int c) {
   return 32 * 128 + r * 32 + (((c - 8) ^ ((r >> 2) & 1)) << 4);
 }
 
+// Two neighbouring outputs, times their gate factors where there are any.
+__device__ __forceinline__ void store_out2(const Kv8AttendArgs& a, size_t at, float x, float y) {
+  if (a.gate) {
+    const float2 g = *reinterpret_cast<const float2*>(a.gate + at);
+    x *= g.x;
+    y *= g.y;
+  }
+  *reinterpret_cast<uint32_t*>(a.out + at) = pack_bf16(x, y);
+}
+
 // A piece of a pair: O[G][hd] (unnormalised), m[G], l[G].
 template <int HD, int G>
 constexpr int kPart = (G * (HD + 2) + 3) & ~3;
@@ -259,7 +269,6 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
         const bool whole = xs >= x0 && xs + nb <= x1, last = it.y < 0;
         float* part = last ? reinterpret_cast<float*>(st_ptr) : ws_warp + w * PART;
         if (!whole && lane == 0) s_piece[2 * w + (x0 < xs)] = 2 * pair + last;
-        bf16* out = a.out + (size_t)pair * G * HD;
         // eu = 0: no block was read
         const float unit = eu ? __uint_as_float((uint32_t)(eu - (int)kShift) << 23) : 0.f;
 #pragma unroll
@@ -278,7 +287,7 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
             for (int d = 0; d < KS; ++d) {
               const int at = head * HD + 16 * d + 2 * g;
               if (whole)
-                *reinterpret_cast<uint32_t*>(out + at) = pack_bf16(o[d][hh] * f, o[d][hh + 2] * f);
+                store_out2(a, (size_t)pair * G * HD + at, o[d][hh] * f, o[d][hh + 2] * f);
               else
                 *reinterpret_cast<float2*>(part + at) =
                     make_float2(o[d][hh] * f, o[d][hh + 2] * f);
@@ -530,10 +539,11 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
       for (int v = 0; v < NV; ++v) {
         const int d = 4 * (lane + 32 * v);
         if (d >= HD) continue;
-        if (whole)
-          *reinterpret_cast<uint2*>(a.out + ((size_t)pr * G + head) * HD + d) =
-              make_uint2(pack_bf16(O[v].x * inv, O[v].y * inv), pack_bf16(O[v].z * inv, O[v].w * inv));
-        else
+        if (whole) {
+          const size_t to = ((size_t)pr * G + head) * HD + d;
+          store_out2(a, to, O[v].x * inv, O[v].y * inv);
+          store_out2(a, to + 2, O[v].z * inv, O[v].w * inv);
+        } else
           *reinterpret_cast<float4*>(part + head * HD + d) = O[v];
       }
       if (!whole && lane == 0) {
@@ -656,8 +666,9 @@ __global__ void kv8_merge_kernel(const Kv8AttendArgs a, int grid, int heads) {
       L = fmaf(f, sl[hh * SP + k], L);
       S = fmaf(f, so[hh * SP + k][d], S);
     }
-    a.out[((size_t)pair * G + blockIdx.y * heads) * HD + i] =
-        __float2bfloat16_rn(L == 0.f ? 0.f : S / L);
+    const size_t to = ((size_t)pair * G + blockIdx.y * heads) * HD + i;
+    const float y = L == 0.f ? 0.f : S / L;
+    a.out[to] = __float2bfloat16_rn(a.gate ? a.gate[to] * y : y);
   }
 }
 

@@ -244,14 +244,6 @@ __global__ void argmax_rows_kernel(const float* z, int V, int* out) {
   block_argmax(v, i, out + r);
 }
 
-// SplitMix64 output function (Steele, Lea and Flood, 2014).
-__device__ __forceinline__ uint64_t splitmix64(uint64_t x) {
-  uint64_t z = x + 0x9E3779B97F4A7C15ull;
-  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
-  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
-  return z ^ (z >> 31);
-}
-
 // Seeded synthetic cache entries for positions [p_lo, p_hi) of one slot:
 // entry (kind, block, slot, b, kvh, pos, j) is the SplitMix64 counter
 // generator's uniform u scaled to (2u - 1) * c_kind and rounded to bf16.
@@ -270,16 +262,7 @@ __global__ void fill_kv_kernel(KVSlot kv, CacheGeo g, int B, int Hkv, int hd,
     const size_t off = kv_index(kv, g, Hkv, hd, b, kvh, pos) + j;
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
-      uint64_t c = (uint64_t)kind;
-      c = c * 64 + (uint64_t)block;
-      c = c * 8 + (uint64_t)slot;
-      c = c * 4096 + (uint64_t)b;
-      c = c * 64 + (uint64_t)kvh;
-      c = c * (1ull << 20) + (uint64_t)pos;
-      c = c * 512 + (uint64_t)j;
-      const uint64_t z = splitmix64(seed + c);
-      const float u = __fmul_rn((float)(z >> 40), 0x1p-24f);
-      const float x = __fmul_rn(__fsub_rn(__fmul_rn(2.f, u), 1.f), kind ? cv : ck);
+      const float x = synthetic_kv(kind, block, slot, b, kvh, pos, j, seed, kind ? cv : ck);
       (kind ? kv.V : kv.K)[off] = __float2bfloat16_rn(x);
     }
   }

@@ -77,7 +77,8 @@ int dory_kv8_append(const dory_kv8* c, const void* d_k, const void* d_v,
   if (!err) return DORY_ERR_CUDA;
   launch_kv8_append(Kv8AppendArgs{to_kv8(c), c->batch, T, (const bf16*)d_k, (const bf16*)d_v,
                                   k_strides[0], k_strides[1], k_strides[2], v_strides[0],
-                                  v_strides[1], v_strides[2], d_pos, d_n, err},
+                                  v_strides[1], v_strides[2], d_pos, d_n, err, nullptr,
+                                  nullptr, 0},
                     (cudaStream_t)stream);
   return launched();
 }
@@ -115,7 +116,7 @@ int dory_kv8_attend(const dory_kv8* c, const void* d_q,
   if (!err || !make_kv8_maps(to_kv8(c), &maps)) return DORY_ERR_CUDA;
   launch_kv8_attend(Kv8AttendArgs{to_kv8(c), c->batch, n_q_heads / c->n_kv_heads,
                                   (const bf16*)d_q, q_strides[0], q_strides[1], d_len, window,
-                                  scale, (bf16*)d_out, d_ws, err},
+                                  scale, (bf16*)d_out, d_ws, err, nullptr},
                     maps, (cudaStream_t)stream);
   return launched();
 }

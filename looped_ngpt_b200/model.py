@@ -11,7 +11,8 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import DoryConfig, DoryTensor, check, KV_MODES
+from ._lib import DoryConfig, DoryTensor, check, KV_FMTS, KV_MODES
+from .ops import sample
 
 
 def _stream_ptr(stream):
@@ -30,26 +31,27 @@ def to_device(arr, device):
 
 
 class KVCache:
-    """A caller-owned device buffer bound as a dory_cache."""
+    """A caller-owned device buffer bound as a dory_cache; kv_fmt "e4m3" holds
+    the full-attention layers' K/V in 8 bits (dory_kv_cache_bind_fmt)."""
 
     def __init__(self, model, batch, max_ctx, max_chunk, max_loops, kv_mode,
-                 stream=None):
+                 stream=None, kv_fmt="bf16"):
         self.model = model
         self.batch, self.max_ctx, self.max_chunk = batch, max_ctx, max_chunk
-        self.kv_mode = kv_mode
+        self.kv_mode, self.kv_fmt = kv_mode, kv_fmt
         lib = _lib.load()
         nbytes = ctypes.c_int64()
-        check("dory_kv_cache_bytes", lib.dory_kv_cache_bytes(
+        check("dory_kv_cache_bytes_fmt", lib.dory_kv_cache_bytes_fmt(
             model.handle, batch, max_ctx, max_chunk, max_loops,
-            KV_MODES[kv_mode], ctypes.byref(nbytes)))
+            KV_MODES[kv_mode], KV_FMTS[kv_fmt], ctypes.byref(nbytes)))
         self.nbytes = nbytes.value
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8,
                                device=model.device)
         h = ctypes.c_void_p()
-        check("dory_kv_cache_bind", lib.dory_kv_cache_bind(
+        check("dory_kv_cache_bind_fmt", lib.dory_kv_cache_bind_fmt(
             model.handle, ctypes.c_void_p(self.buf.data_ptr()), self.nbytes,
             batch, max_ctx, max_chunk, max_loops, KV_MODES[kv_mode],
-            _stream_ptr(stream), ctypes.byref(h)))
+            KV_FMTS[kv_fmt], _stream_ptr(stream), ctypes.byref(h)))
         self.handle = h
 
     def length(self):
@@ -119,9 +121,9 @@ class DoryModel:
 
     # ---- buffers ---------------------------------------------------------
     def new_cache(self, batch, max_ctx, max_chunk, kv_mode="last_loop",
-                  max_loops=4, stream=None):
+                  max_loops=4, stream=None, kv_fmt="bf16"):
         return KVCache(self, batch, max_ctx, max_chunk, max_loops, kv_mode,
-                       stream)
+                       stream, kv_fmt)
 
     def workspace(self, batch, max_chunk):
         n = ctypes.c_int64()
@@ -176,6 +178,44 @@ class DoryModel:
             ctypes.c_void_p(argmax.data_ptr()), ctypes.c_void_p(ws.data_ptr()),
             ws.numel(), _stream_ptr(stream)))
         return logits, argmax
+
+    def generate(self, prompt, n_new, n_loops, temperature=0.0, top_k=0,
+                 top_p=1.0, min_p=0.0, uniform=None, kv_mode="last_loop",
+                 kv_fmt="bf16", logprobs=False):
+        """Prefill the prompt (device int32 [B, T]) and append n_new tokens per
+        sequence, each drawn by dory_sample from the logits of the last one
+        (temperature 0: greedy).  temperature, top_k, top_p and min_p are
+        numbers or device tensors [B].  uniform: f32 [n_new, B] in [0, 1), or
+        None to draw it from torch's generator.  Returns the new tokens int32
+        [B, n_new], and their log-probabilities f32 [B, n_new] if `logprobs`.
+        Runs on the current stream and waits for it once, at the end."""
+        B, T = prompt.shape
+        dev = prompt.device
+
+        def option(x, dtype):
+            if isinstance(x, torch.Tensor):
+                return x
+            return torch.full((B,), x, dtype=dtype, device=dev)
+
+        opts = dict(temperature=option(temperature, torch.float32),
+                    top_k=option(top_k, torch.int32),
+                    top_p=option(top_p, torch.float32),
+                    min_p=option(min_p, torch.float32))
+        if uniform is None:
+            uniform = torch.rand((n_new, B), device=dev)
+        tokens = torch.empty((n_new, B), dtype=torch.int32, device=dev)
+        lps = torch.empty((n_new, B), dtype=torch.float32, device=dev)
+        cache = self.new_cache(B, T + n_new, T, kv_mode=kv_mode,
+                               max_loops=n_loops, kv_fmt=kv_fmt)
+        ws = self.workspace(B, T)
+        logits, _ = self.prefill(cache, prompt, n_loops, ws)
+        for i in range(n_new):
+            if i:
+                logits, _ = self.decode_step(cache, tokens[i - 1], n_loops, ws)
+            sample(logits, uniform[i], tokens=tokens[i], logprobs=lps[i], **opts)
+        tokens, lps = tokens.t().contiguous(), lps.t().contiguous()
+        torch.cuda.current_stream(dev).synchronize()   # before the cache goes
+        return (tokens, lps) if logprobs else tokens
 
     def prefill_mixed(self, cache, tokens, row_loops, ws, logits_all=False,
                       stream=None):

@@ -9,6 +9,7 @@ older rows are brought to the scale in the same way.
 """
 import numpy as np
 
+from .model import DT, Model
 from .quant import e4m3_decode, round_e4m3
 
 BLOCK = 32
@@ -65,3 +66,44 @@ def attend(q, k, v, window, scale):
     p = np.exp(z - z.max(1, keepdims=True))
     p /= p.sum(1, keepdims=True)
     return p @ v[lo:], p @ np.abs(v[lo:])
+
+
+def round_bf16(x):
+    """Nearest bf16 values, ties to even (finite x)."""
+    u = np.asarray(x, dtype=np.float32).view(np.uint32).astype(np.uint64)
+    u = (u + 0x7FFF + ((u >> 16) & 1)) & 0xFFFF0000
+    return u.astype(np.uint32).view(np.float32).astype(DT)
+
+
+class Kv8Model(Model):
+    """The looped model whose full-attention layers hold their K/V in 8 bits:
+    a call's rows (rounded to bf16, what a bf16 cache holds) are appended to
+    the layer's codes, then every query reads the decoded values.  jitter:
+    relative size of a random change of every k and v before they are stored,
+    to measure how much the stored codes depend on it."""
+
+    def __init__(self, *args, jitter=0.0, **kw):
+        super().__init__(*args, **kw)
+        self.codes, self.jitter = {}, jitter
+        self.rng = np.random.default_rng(99)
+
+    def store_kv(self, i, slot, pos, k, v):
+        K, V = super().store_kv(i, slot, pos, k, v)
+        if self.shape.layer_types[i] != 1:
+            return K, V
+        end = int(pos[-1]) + 1
+        cap = -(-end // BLOCK) * BLOCK
+        for kind, (x, out) in enumerate(((k, K), (v, V))):
+            x = x * (1 + self.jitter * self.rng.uniform(-1, 1, x.shape))
+            for b in range(x.shape[0]):
+                for h in range(x.shape[1]):
+                    c, s = self.codes.get((i, slot, kind, b, h),
+                                          (np.zeros((0, x.shape[-1]), np.uint8),
+                                           np.zeros(0)))
+                    if len(c) < cap:
+                        c = np.concatenate([c, np.zeros((cap - len(c), c.shape[1]), np.uint8)])
+                        s = np.concatenate([s, np.zeros(cap // BLOCK - len(s))])
+                    self.codes[i, slot, kind, b, h] = c, s
+                    append(c, s, int(pos[0]), round_bf16(x[b, h]))
+                    out[b, h, :end] = decode(c, s, end)
+        return K, V

@@ -212,6 +212,14 @@ class Model:
             self.cache[key] = (K, V)
         return self.cache[key]
 
+    def store_kv(self, i, slot, pos, k, v):
+        """Store the call's k, v [B, Hkv, T, h] at positions pos; returns the
+        slot's K, V arrays as the queries read them."""
+        K, V = self.slot_arrays(i, slot, int(pos[-1]) + 1)
+        K[:, :, pos] = k
+        V[:, :, pos] = v
+        return K, V
+
     def kv_slots(self):
         """Distinct (block, slot) caches in use."""
         return sorted(self.cache)
@@ -235,9 +243,7 @@ class Model:
         q = s_q * l2n(rope(q, pos, theta))
         k = s_k * l2n(rope(k, pos, theta))
         end = int(pos[-1]) + 1
-        K, V = self.slot_arrays(i, slot, end)
-        K[:, :, pos] = k
-        V[:, :, pos] = v
+        K, V = self.store_kv(i, slot, pos, k, v)
         kpos = np.arange(end)
         window = 0 if full else sh.swa_window
         o = np.stack([attention(q[b], K[b, :, :end], V[b, :, :end], pos, kpos,

@@ -84,3 +84,35 @@ def test_attend_closed_forms():
     assert np.allclose(o, v[3:].mean(0))
     o, _ = kv8.attend(q, k[:0], v[:0], 0, 1.0)
     assert np.all(o == 0)
+
+
+def test_kv8_model_holds_codes_and_stays_near_the_model():
+    """Sliding-window layers are untouched; a full layer's entries are the
+    decoded codes of the bf16 rows; an 8-bit cache changes logits, but little;
+    and decoding token by token equals one call up to a subnormal step."""
+    from oracle import Model
+    from synthetic import TINY, make_prompt, make_weights
+    w = make_weights(TINY, seed=0)
+    toks = make_prompt(TINY, 1, 70)
+    ref = Model(TINY, w, kv_mode="per_loop")
+    z0 = ref.forward(toks, 2, all_logits=True)
+    m = kv8.Kv8Model(TINY, w, kv_mode="per_loop")
+    z1 = m.forward(toks, 2, all_logits=True)
+    d = np.abs(z1 - z0).max()
+    assert 1e-4 < d < 0.2
+    full = [i for i, t in enumerate(TINY.layer_types) if t == 1]
+    assert {k[0] for k in m.codes} == set(full) and full
+    (i, slot, kind, b, h), (c, s) = next(iter(m.codes.items()))
+    assert np.array_equal(m.cache[i, slot][kind][b, h, :70], kv8.decode(c, s, 70))
+    m2 = kv8.Kv8Model(TINY, w, kv_mode="per_loop")
+    m2.forward(toks[:, :37], 2)
+    for t in range(37, 70):
+        z = m2.decode_step(toks[:, t], 2)
+    assert np.abs(z - z1[:, -1]).max() < d
+
+
+def test_round_bf16():
+    x = np.array([1.0, 1.00390625, 1.01171875, -3.14159, 1e-3])
+    import torch
+    want = torch.tensor(x, dtype=torch.float32).to(torch.bfloat16).double().numpy()
+    assert np.array_equal(kv8.round_bf16(x), want)
