@@ -23,14 +23,19 @@ namespace {
 // new rows become RNE codes of x / s (NaN stays NaN, infinities saturate),
 // older rows are brought to s if it grew; rows behind the new ones are left
 // as they are.
-constexpr int kAppThreads = 128;
-
+//
+// HBM-bound (2 bytes read, 1 written per element), if few instructions are
+// spent on 8 elements: 8 row groups x one 16-byte chunk per thread, so that a
+// thread's four chunks are 8 rows apart; magnitudes are compared as packed
+// 16-bit integers, and again without infinities and NaN only where there are
+// some.  The rows are asked for before the page number has arrived.
 template <int HD, bool PAGED>
-__global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(Kv8AppendArgs a) {
-  constexpr int CH = HD / 8;                   // 8-element chunks per row
-  constexpr int N = (kKv8Block * CH + kAppThreads - 1) / kAppThreads;
-  __shared__ uint32_t s_amax;
-  const int b = blockIdx.z, h = blockIdx.y, kind = blockIdx.x & 1;
+__global__ void __launch_bounds__(HD) kv8_append_kernel(Kv8AppendArgs a) {
+  constexpr int CH = HD / 8, NT = HD;          // 16-byte chunks per row; threads
+  constexpr int N = kKv8Block / 8;             // rows per thread
+  __shared__ uint32_t s_amax[NT / 32];
+  const int b = blockIdx.z, h = blockIdx.y, kind = blockIdx.x & 1, tid = threadIdx.x;
+  const int rt = tid / CH, c = tid - rt * CH;  // rows rt, rt + 8, ..; chunk
   pdl_wait();
   pdl_trigger();
   int pos, n;
@@ -43,62 +48,72 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(Kv8AppendArgs a
   }
   if (n == 0) return;
   if (pos < 0 || n < 0 || n > a.T || pos > a.c.pages_per_seq * kPage - n) {
-    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) atomicOr(a.err, ERRBIT_BOUNDS);
+    if (blockIdx.x == 0 && h == 0 && tid == 0) atomicOr(a.err, ERRBIT_BOUNDS);
     return;
   }
   const int j = pos / kKv8Block + (blockIdx.x >> 1);      // block of the sequence
   const int p0 = j * kKv8Block;
   if (p0 >= pos + n) return;
-  const int page = a.c.block_table[(size_t)b * a.c.pages_per_seq + p0 / kPage];
-  if (page < 0 || page >= a.c.n_pages) {
-    if (threadIdx.x == 0) atomicOr(a.err, ERRBIT_BOUNDS);
+  const int r0 = max(0, pos - p0), r1 = min(kKv8Block, pos + n - p0);  // new rows
+  const int half = j & 1;
+  const int* entry = a.c.block_table + (size_t)b * a.c.pages_per_seq + p0 / kPage;
+  auto unit_of = [&](int page) { return ((size_t)page * a.c.Hkv + h) * 2 + half; };
+
+  uint4 x[N];
+  int page;
+  auto load = [&](const bf16* src, int64_t st) {          // row r at src + r st
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = rt + 8 * i;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (r >= r0 && r < r1) x[i] = *reinterpret_cast<const uint4*>(src + r * st + 8 * c);
+    }
+  };
+  if (PAGED) {
+    page = *entry;
+    load((kind ? a.v : a.k) + unit_of(page) * kKv8Block * HD, HD);
+  } else {
+    const int64_t st = kind ? a.vs_t : a.ks_t;
+    load((kind ? a.v : a.k) + b * (kind ? a.vs_b : a.ks_b) + h * (kind ? a.vs_h : a.ks_h) +
+             (int64_t)(p0 - pos) * st, st);
+    page = *entry;
+  }
+  if (page < 0 || page >= a.c.n_pages) {       // the same for the whole block
+    if (tid == 0) atomicOr(a.err, ERRBIT_BOUNDS);
     return;
   }
-  const size_t ph = (size_t)page * a.c.Hkv + h;
-  const int half = (p0 / kKv8Block) & 1;
-  uint8_t* codes = (kind ? a.c.v : a.c.k) + (ph * kPage + half * kKv8Block) * HD;
-  float* scale = (kind ? a.c.v_scale : a.c.k_scale) + ph * 2 + half;
-  // row r of the block is src + r st
-  const bf16* src = kind ? a.v : a.k;
-  int64_t st = kind ? a.vs_t : a.ks_t;
-  if (PAGED) {
-    src += (ph * kPage + half * kKv8Block) * HD;
-    st = HD;
-  } else {
-    src += b * (kind ? a.vs_b : a.ks_b) + h * (kind ? a.vs_h : a.ks_h) + (int64_t)(p0 - pos) * st;
-  }
-  const int r0 = max(0, pos - p0), r1 = min(kKv8Block, pos + n - p0);  // new rows
+  const size_t unit = unit_of(page);
+  uint8_t* codes = (kind ? a.c.v : a.c.k) + unit * kKv8Block * HD + rt * HD + 8 * c;
+  float* scale = (kind ? a.c.v_scale : a.c.k_scale) + unit;
+  const float s_old = r0 > 0 ? *scale : 0.f;
 
-  if (threadIdx.x == 0) s_amax = 0;
-  __syncthreads();
-  uint4 x[N];
-  uint32_t mx = 0;
+  uint32_t mx = 0;                             // two bf16 magnitudes
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = threadIdx.x + i * kAppThreads, r = e / CH, c = e - r * CH;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (r >= r0 && r < r1) {
-      x[i] = *reinterpret_cast<const uint4*>(src + r * st + 8 * c);
-      mx = max(max(mx, kv8_amax2(x[i].x)), max(kv8_amax2(x[i].y),
-               max(kv8_amax2(x[i].z), kv8_amax2(x[i].w))));
-    }
+  for (int i = 0; i < N; ++i)
+    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                               __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+  mx = max(mx & 0xffff0000u, mx << 16);        // the larger, as f32 bits
+  if (mx >= 0x7f800000u) {                     // without what is not finite
+    mx = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      mx = max(mx, max(max(kv8_amax2(x[i].x), kv8_amax2(x[i].y)),
+                       max(kv8_amax2(x[i].z), kv8_amax2(x[i].w))));
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
-  if ((threadIdx.x & 31) == 0) atomicMax(&s_amax, mx);
-  __syncthreads();
-  const float s_old = r0 > 0 ? *scale : 0.f;
-  const float s = fmaxf(s_old, kv8_scale_for(s_amax));
+  if ((tid & 31) == 0) s_amax[tid >> 5] = mx;
+  __syncthreads();                             // (and s_old has been read)
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) mx = max(mx, s_amax[i]);
+  const float s = fmaxf(s_old, kv8_scale_for(mx));
   const float inv = kv8_inv(s);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int e = threadIdx.x + i * kAppThreads, r = e / CH, c = e - r * CH;
-    if (r >= r0 && r < r1)
-      *reinterpret_cast<uint2*>(codes + r * HD + 8 * c) = kv8_encode8(x[i], inv);
-    else if (r < r0 && s != s_old)
-      kv8_rescale8(codes + r * HD + 8 * c, s_old, inv);
+    const int r = rt + 8 * i;
+    if (r >= r0 && r < r1) *reinterpret_cast<uint2*>(codes + 8 * i * HD) = kv8_encode8(x[i], inv);
+    else if (r < r0 && s != s_old) kv8_rescale8(codes + 8 * i * HD, s_old, inv);
   }
-  __syncthreads();                             // every thread has read s_old
-  if (threadIdx.x == 0) *scale = s;
+  if (tid == 0) *scale = s;
 }
 
 // ------------------------------------------------------- one-token calls ----
@@ -254,8 +269,8 @@ __global__ void __launch_bounds__(256) kv8_copy_prefix_kernel(Kv8 src, int src_b
 
 template <int HD>
 void append_hd(const Kv8AppendArgs& a, dim3 grid, cudaStream_t st) {
-  if (a.pos) launch_k(kv8_append_kernel<HD, false>, grid, dim3(kAppThreads), 0, st, a);
-  else launch_k(kv8_append_kernel<HD, true>, grid, dim3(kAppThreads), 0, st, a);
+  if (a.pos) launch_k(kv8_append_kernel<HD, false>, grid, dim3(HD), 0, st, a);
+  else launch_k(kv8_append_kernel<HD, true>, grid, dim3(HD), 0, st, a);
 }
 
 template <int HD>

@@ -49,10 +49,18 @@ __device__ __forceinline__ uint32_t kv8_f16x2(uint32_t codes) {
 
 // Eight bf16 values times inv -> eight codes.
 __device__ __forceinline__ uint2 kv8_encode8(const uint4& x, float inv) {
-  auto two = [&](uint32_t u) {
-    return kv8_encode2(__uint_as_float(u << 16) * inv, __uint_as_float(u & 0xffff0000u) * inv);
+  auto four = [&](uint32_t u, uint32_t v) {
+    uint32_t r;
+    asm("{\n .reg .b16 l, h;\n"
+        " cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
+        " cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
+        " mov.b32 %0, {l, h};\n}"
+        : "=r"(r)
+        : "f"(__uint_as_float(u << 16) * inv), "f"(__uint_as_float(u & 0xffff0000u) * inv),
+          "f"(__uint_as_float(v << 16) * inv), "f"(__uint_as_float(v & 0xffff0000u) * inv));
+    return r;
   };
-  return make_uint2(two(x.x) | two(x.y) << 16, two(x.z) | two(x.w) << 16);
+  return make_uint2(four(x.x, x.y), four(x.z, x.w));
 }
 
 // Eight codes of scale s_old to the scale whose inverse is inv, in place.
