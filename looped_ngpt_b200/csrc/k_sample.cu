@@ -107,7 +107,8 @@ struct Cand {
 //                          ran 17 times slower); then the own candidates
 //   zs    f32 [per]        the slice
 //   bins  u32 [][threads]  bins of each thread's logits in the first histogram,
-//                          four to a word
+//                          four to a word; later all kept logits, Cand [C][gc],
+//                          written by the row's blocks, where there are few
 // A buffer that other blocks write is written again only after a barrier that
 // follows its last read.
 struct Fixed {
@@ -115,6 +116,7 @@ struct Fixed {
     uint32_t max[kMaxC], min[kMaxC];   // integer images
     int g_n[kMaxC];
     uint32_t g_min[kMaxC], g_max[kMaxC];
+    int l_n[kMaxC];
     int tie;
     double sum[kMaxC];
   } ex;
@@ -135,11 +137,16 @@ static_assert(sizeof(Fixed) % 16 == 0, "what follows is 16-byte aligned");
 
 // Candidates per block: few blocks may send more each.
 __host__ __device__ inline int cand_cap(int C) { return C >= 4 ? 32 : kRank / C; }
+__host__ __device__ inline size_t bins_bytes(int C, int per) {
+  const size_t bins = (size_t)(per / kSampThreads + 3) / 4 * kSampThreads * 4;
+  const size_t list = (size_t)C * cand_cap(C) * sizeof(Cand);
+  return bins > list ? bins : list;
+}
 __host__ __device__ inline size_t sample_smem(int C, int per) {
   return sizeof(Fixed) + (size_t)C * kNB * 8 + (size_t)C * cand_cap(C) * sizeof(Cand) +
-         kHistWords * 4 + (size_t)per * 4 + (size_t)(per / kSampThreads + 3) / 4 * kSampThreads * 4;
+         kHistWords * 4 + (size_t)per * 4 + bins_bytes(C, per);
 }
-static_assert(kRank * sizeof(Cand) <= kHistWords * 4, "candidates fit the histograms' place");
+static_assert(kRank * (2 * sizeof(Cand) + 8) <= kHistWords * 4, "lists fit the histograms' place");
 
 __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, int C, int pw) {
   extern __shared__ __align__(16) uint8_t smraw[];
@@ -162,9 +169,9 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   pdl_trigger();
   const float* z = a.logits + (size_t)row * a.ld;
   const float T = a.temperature ? a.temperature[row] : 1.f;
-  const bool greedy = !(T > 0.f);
   int k = a.top_k ? a.top_k[row] : 0;
   if (k <= 0 || k > a.V) k = a.V;
+  const bool greedy = !(T > 0.f) || k == 1;
   float minp = a.min_p ? a.min_p[row] : 0.f, topp = a.top_p ? a.top_p[row] : 1.f;
   minp = minp > 0.f ? fminf(minp, 1.f) : 0.f;
   const float uf = a.uniform[row];
@@ -256,13 +263,35 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   // Logits below `floor` weigh nothing: less than e^-44 of the largest, 2^-46
   // of the mass for all of a row.
   const float floor = m - 44.f * T;
-  // (free of branches, so that kU of them overlap; for v >= floor)
-  auto weight = [&](float v) -> double { return exp2_16th(((double)v - md) * rate, s.tab); };
+  // y = 16 log2(e) (v - m) / T, in one fma where its rounding error, 2^-53 of
+  // m's share, is below 2^-37: |m| / T up to 4096
+  const bool near0 = fabsf(m) <= 4096.f * T;
+  const double y0 = -md * rate;
+  // N at a time, free of branches, so that they overlap; for v >= floor
+  auto weights = [&](auto& x, const auto& v) {
+    constexpr int N = sizeof(v) / sizeof(v[0]);
+    if (near0) {
+#pragma unroll
+      for (int u = 0; u < N; ++u) x[u] = fma((double)v[u], rate, y0);
+    } else {
+#pragma unroll
+      for (int u = 0; u < N; ++u) x[u] = ((double)v[u] - md) * rate;
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) x[u] = exp2_16th(x[u], s.tab);
+  };
+  auto weight = [&](float v) -> double {
+    const float one[1] = {v};
+    double x[1];
+    weights(x, one);
+    return x[0];
+  };
   // weights as integers of 43 bits, nearest (adding 2^52 leaves them in the
   // low bits of the double)
-  auto fixed = [&](float v) -> u64 {
-    return (u64)__double_as_longlong(fma(weight(v), 0x1p43, 0x1p52)) & 0xfffffffffffffull;
+  auto as_fixed = [&](double x) -> u64 {
+    return (u64)__double_as_longlong(fma(x, 0x1p43, 0x1p52)) & 0xfffffffffffffull;
   };
+  auto fixed = [&](float v) { return as_fixed(weight(v)); };
 
   // kept: z > cz, or z == cz and index <= ci
   float cz = -INFINITY;
@@ -302,11 +331,16 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     uint32_t mask = 0;                 // this thread's logits still in question
     for (int level = 0;; ++level) {
       // histogram of the kept logits in [low, hi]
-      const double hd = (double)hi, sc = low == hi ? 0.0 : (double)kNB / (hd - (double)low);
       // bin of (hi - v) sc, rounded (monotone; the ends fall into the first and
-      // the last bin)
+      // the last bin): in f32, or in f64 where the range of
+      // the logits or its reciprocal leaves f32's
+      const float span = hi - low;
+      const bool f32 = span > 1e-30f && span < 1e30f;
+      const float sf = f32 ? (float)kNB / span : 0.f;
+      const double hd = (double)hi, sc = low == hi ? 0.0 : (double)kNB / (hd - (double)low);
       auto bin_of = [&](float v) {
-        const int q = __double2loint(fma(hd - (double)v, sc, 0x1.8p52 - 0.5));
+        const int q = f32 ? __float_as_int(fmaf(hi - v, sf, 0x1.8p23f - 0.5f)) - 0x4b400000
+                          : __double2loint(fma(hd - (double)v, sc, 0x1.8p52 - 0.5));
         return max(0, min(q, kNB - 1));
       };
       __syncthreads();
@@ -339,10 +373,12 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
           if (__any_sync(0xffffffffu, in)) {
             int bn[kU];
             u64 f[kU];
+            double x[kU];
+            if (by_mass) weights(x, v);
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
               bn[u] = bin_of(v[u]);
-              f[u] = by_mass ? fixed(v[u]) : 1;
+              f[u] = by_mass ? as_fixed(x[u]) : 1;
             }
 #pragma unroll
             for (int u = 0; u < kU; ++u)
@@ -549,6 +585,127 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     cut = true;
     lo = fmaxf(lo, cz);
   }
+  // ---- few kept: every block gets them all, and decides without the rest -----
+  if (k <= kRank) {
+    uint32_t mask = 0;
+    for (int q = 0; q < run; ++q) {
+      const int i = i0 + 32 * q;
+      const float v = zs[i];
+      mask |= (uint32_t)(v >= floor && (v > cz || (v == cz && base + i <= ci))) << q;
+    }
+    __syncthreads();
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+    const int mine = __popc(mask), warps = __reduce_add_sync(0xffffffffu, mine);
+    int at = 0;
+    if (warps) {
+      if (lane == 0) at = atomicAdd(&s.n, warps);
+      at = __shfl_sync(0xffffffffu, at, 0);
+      int inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      at += inc - mine;
+      for (uint32_t r = mask; r; r &= r - 1, ++at) {
+        const int i = i0 + 32 * (__ffs(r) - 1);
+        if (at < gc) own_cand[at] = Cand{zs[i], base + i, (u64)__double_as_longlong(weight(zs[i]))};
+      }
+    }
+    __syncthreads();
+    const int own = s.n, send = own <= gc ? own : 0;
+    Cand* ex_list = reinterpret_cast<Cand*>(bins - tid);
+    if (tid < C) put32(&s.ex.l_n[rank], tid, own);
+    for (int i = tid; i < C * send; i += kSampThreads) {
+      const int c = i / send, j = i - c * send;
+      const Cand x = own_cand[j];
+      Cand* to = ex_list + rank * gc + j;
+      put32(&to->z, c, __float_as_uint(x.z));
+      put32(&to->i, c, x.i);
+      put64(&to->w, c, x.w);
+    }
+    cluster_sync_all();
+    const int ln = lane < C ? s.ex.l_n[lane] : 0;
+    const int n = __reduce_add_sync(0xffffffffu, ln);
+    if (n <= kRank && __all_sync(0xffffffffu, ln <= gc)) {
+      if (rank) return;
+      Cand* list = own_cand;                          // as they came
+      Cand* by_index = list + kRank;
+      double* kw = reinterpret_cast<double*>(by_index + kRank);
+      for (int e = tid; e < C * gc; e += kSampThreads) {
+        const int c = e / gc, j = e - c * gc;
+        if (j < s.ex.l_n[c]) {
+          int to = j;
+          for (int q = 0; q < c; ++q) to += s.ex.l_n[q];
+          list[to] = ex_list[e];
+        }
+      }
+      __syncthreads();
+      if (tid < n) {
+        const Cand me = list[tid];
+        int to = 0;
+#pragma unroll 4
+        for (int q = 0; q < n; ++q) to += list[q].i < me.i;
+        by_index[to] = me;
+      }
+      __syncthreads();
+      if (tid < n) {
+        // mass before it by (z, index), and of all
+        const Cand me = by_index[tid];
+        double before = 0.0, all = 0.0;
+        bool first = true;
+#pragma unroll 4
+        for (int q = 0; q < n; ++q) {
+          const Cand o = by_index[q];
+          const double x = __longlong_as_double((long long)o.w);
+          const bool b = o.z > me.z || (o.z == me.z && q < tid);
+          all += x;
+          before += b ? x : 0.0;
+          first = first && !b;
+        }
+        const bool in = !(topp < 1.f) || first || before < (double)topp * all;
+        kw[tid] = in ? __longlong_as_double((long long)me.w) : 0.0;
+      }
+      __syncthreads();
+      if (w == 0) {
+        // running mass in index order, four neighbours per lane
+        double x[kRank / 32], sum = 0.0;
+#pragma unroll
+        for (int u = 0; u < kRank / 32; ++u) {
+          const int e = kRank / 32 * lane + u;
+          x[u] = e < n ? kw[e] : 0.0;
+          sum += x[u];
+        }
+        double inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        const double total = __shfl_sync(0xffffffffu, inc, 31);
+        const double target = (uf > 0.f ? fmin((double)uf, 1.0) : 0.0) * total;
+        const unsigned any = __ballot_sync(0xffffffffu, sum > 0.0);
+        const unsigned hit = __ballot_sync(0xffffffffu, sum > 0.0 && inc > target);
+        if (lane == (hit ? __ffs(hit) - 1 : 31 - __clz(any))) {
+          double c = inc - sum;
+          int pick = -1;
+#pragma unroll
+          for (int u = 0; u < kRank / 32; ++u)
+            if (x[u] > 0.0 && (pick < 0 || !(c > target))) {
+              pick = kRank / 32 * lane + u;
+              c += x[u];
+            }
+          const Cand me = by_index[pick];
+          a.tokens[row] = me.i;
+          if (a.logprobs)
+            a.logprobs[row] =
+                (float)((me.z == m ? 0.0 : ((double)me.z - md) * inv_t) - log(total));
+        }
+      }
+      return;
+    }
+  }
   if (topp < 1.f) select(true);
 
   // ---- the draw ---------------------------------------------------------------
@@ -569,7 +726,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     if (!__any_sync(0xffffffffu, any)) continue;
     double x[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) x[u] = weight(in[u] ? v[u] : m);
+    for (int u = 0; u < kU; ++u) v[u] = in[u] ? v[u] : m;
+    weights(x, v);
 #pragma unroll
     for (int u = 0; u < kU; ++u) sum += in[u] ? x[u] : 0.0;
   }
