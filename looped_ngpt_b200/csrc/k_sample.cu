@@ -25,6 +25,8 @@
 #include "async_copy.cuh"
 #include "common.cuh"
 
+#include <cfloat>
+
 namespace dory {
 
 namespace {
@@ -105,7 +107,8 @@ struct Cand {
 //                          of the weights, whose sums over up to 1024 logits
 //                          stay below 2^32 (64-bit atomics on shared memory
 //                          ran 17 times slower); then the own candidates
-//   zs    f32 [per]        the slice
+//   zs    f32 [per + 4]    the slice, shifted so that 16-byte chunks of the row
+//                          stay 16-byte aligned
 //   bins  u32 [][threads]  bins of each thread's logits in the first histogram,
 //                          four to a word; later all kept logits, Cand [C][gc],
 //                          written by the row's blocks, where there are few
@@ -144,7 +147,7 @@ __host__ __device__ inline size_t bins_bytes(int C, int per) {
 }
 __host__ __device__ inline size_t sample_smem(int C, int per) {
   return sizeof(Fixed) + (size_t)C * kNB * 8 + (size_t)C * cand_cap(C) * sizeof(Cand) +
-         kHistWords * 4 + (size_t)per * 4 + bins_bytes(C, per);
+         kHistWords * 4 + (size_t)(per + 4) * 4 + bins_bytes(C, per);
 }
 static_assert(kRank * (2 * sizeof(Cand) + 8) <= kHistWords * 4, "lists fit the histograms' place");
 
@@ -156,13 +159,13 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   Cand* ex_cand = reinterpret_cast<Cand*>(ex_mass + C * kNB);
   uint32_t* hist_all = reinterpret_cast<uint32_t*>(ex_cand + C * gc);
   Cand* own_cand = reinterpret_cast<Cand*>(hist_all);
-  float* zs = reinterpret_cast<float*>(hist_all + kHistWords);
+  float* zs0 = reinterpret_cast<float*>(hist_all + kHistWords);
   const int row = blockIdx.x / C, rank = blockIdx.x - row * C;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = kSW * pw, base = rank * per;      // this block's slice
   const int i0 = w * pw + lane, i1 = w * pw + pw;   // this thread's logits: i0, i0 + 32, ..
-  uint32_t* bins = reinterpret_cast<uint32_t*>(zs + per) + tid;
-  const int run = pw / 32;                          // logits per thread, at most 32
+  uint32_t* bins = reinterpret_cast<uint32_t*>(zs0 + per + 4) + tid;
+  const int run = pw / 32;                          // logits per thread: 4 .. 32, a multiple of kU
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if (tid < 16) s.tab[tid] = kExpTab[tid];
   pdl_wait();
@@ -177,37 +180,55 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   const float uf = a.uniform[row];
 
   // ---- the slice, its largest and smallest finite logit ---------------------
-  // (4-byte copies: rows need no alignment), in four parts, so that the first
-  // are looked at while the others arrive
-  const int part = (run + 3) / 4 * 32;
+  // In four parts, so that the first are looked at while the others arrive: a
+  // thread looks at the chunks it copied.
+  const float* src = z + base;
+  const int cnt = max(0, min(per, a.V - base));
+  const int shift = (int)((uintptr_t)src >> 2) & 3, head = min((4 - shift) & 3, cnt);
+  float* zs = zs0 + shift;
+  const int chunks = (cnt - head) / 4, tail = head + 4 * chunks;
+  if (tid < head) zs[tid] = src[tid];
+  if (tid < cnt - tail) zs[tail + tid] = src[tail + tid];
+  for (int i = cnt + tid; i < per; i += kSampThreads) zs[i] = -INFINITY;
+  const int rounds = (chunks + kSampThreads - 1) / kSampThreads, part = (rounds + 3) / 4;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    for (int i = i0 + g * part; i < min(i1, i0 + (g + 1) * part); i += 32) {
-      if (base + i < a.V)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(su32(zs + i)),
-                     "l"(z + base + i)
+    for (int t = g * part; t < (g + 1) * part; ++t) {
+      const int i = tid + t * kSampThreads;
+      if (i < chunks)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(su32(zs + head + 4 * i)),
+                     "l"(src + head + 4 * i)
                      : "memory");
-      else
-        zs[i] = -INFINITY;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   float vmax = -INFINITY, vmin = INFINITY;          // of what may be drawn
+  auto look = [&](float v) {
+    vmax = fmaxf(vmax, v);                          // (passes over NaN)
+    if (k < a.V && v > -INFINITY) vmin = fminf(vmin, v);
+  };
+  if (tid < head) look(src[tid]);
+  if (tid < cnt - tail) look(src[tail + tid]);
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     if (g == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
     if (g == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
     if (g == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
     if (g == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    for (int i = i0 + g * part; i < min(i1, i0 + (g + 1) * part); i += 32) {
-      const float v = zs[i];
-      vmax = fmaxf(vmax, v);                        // (passes over NaN)
-      vmin = v > -INFINITY ? fminf(vmin, v) : vmin;
+    for (int t = g * part; t < (g + 1) * part; ++t) {
+      const int i = tid + t * kSampThreads;
+      if (i < chunks) {
+        const float4 v = *reinterpret_cast<const float4*>(zs + head + 4 * i);
+        look(v.x);
+        look(v.y);
+        look(v.z);
+        look(v.w);
+      }
     }
   }
   // integer images (+ 0.f: -0 as +0)
   uint32_t kmax = vmax > -INFINITY ? key_of(vmax + 0.f) : 0u;
-  uint32_t kmin = vmax > -INFINITY ? key_of(vmin + 0.f) : 0xffffffffu;
+  uint32_t kmin = vmin < INFINITY ? key_of(vmin + 0.f) : 0xffffffffu;
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   if (lane == 0) {
@@ -235,7 +256,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     }
     return;
   }
-  float m = key_float(kmax), lo = key_float(kmin);
+  // lo: the smallest logit where a top-k may need it, else -inf
+  float m = key_float(kmax), lo = k < a.V ? fminf(m, key_float(kmin)) : -INFINITY;
   if (greedy) {
     // the lowest index of the largest logit, in the first block that has it
     const unsigned has = __ballot_sync(0xffffffffu, lane < C && s.ex.max[lane] == kmax);
@@ -325,7 +347,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   auto select = [&](const bool by_mass) {
     float hi = m, low = lo;
     // below m - 31 T integer weights are 0
-    if (by_mass) low = fmaxf(low, m - 31.f * T);
+    if (by_mass) low = fmaxf(fmaxf(low, m - 31.f * T), -FLT_MAX);
     low = fminf(low, hi);
     u64 mass_above = 0, want = 0;      // weights, or logits, before and up to the cutoff
     uint32_t mask = 0;                 // this thread's logits still in question
@@ -364,10 +386,9 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
             const int i = i0 + 32 * (q + u);
-            v[u] = q + u < run ? zs[i] : -INFINITY;
-            bool ok = v[u] >= low;
-            if (cut) ok = ok && (v[u] > cz || (v[u] == cz && base + i <= ci));
-            in |= (uint32_t)ok << u;
+            v[u] = zs[i];
+            in |= (uint32_t)(v[u] >= low) << u;
+            if (cut && v[u] <= cz && !(v[u] == cz && base + i <= ci)) in &= ~(1u << u);
           }
           uint32_t word = 0xffffffffu;
           if (__any_sync(0xffffffffu, in)) {
@@ -706,7 +727,10 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       return;
     }
   }
-  if (topp < 1.f) select(true);
+  if (topp < 1.f) {
+    select(true);
+    cut = true;
+  }
 
   // ---- the draw ---------------------------------------------------------------
   // weight of logit i of the slice, 0 if it is not kept
@@ -719,15 +743,14 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int i = i0 + 32 * (q + u);
-      v[u] = q + u < run ? zs[i] : -INFINITY;
-      in[u] = kept(v[u], i);
+      v[u] = zs[i];
+      in[u] = v[u] >= from;
+      if (cut && v[u] == cz && base + i > ci) in[u] = false;
       any |= in[u];
     }
     if (!__any_sync(0xffffffffu, any)) continue;
     double x[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) v[u] = in[u] ? v[u] : m;
-    weights(x, v);
+    weights(x, v);                     // (of anything where `in` is false)
 #pragma unroll
     for (int u = 0; u < kU; ++u) sum += in[u] ? x[u] : 0.0;
   }
@@ -1013,7 +1036,7 @@ void launch_sample(const SampleArgs& a, cudaStream_t st) {
     launch_k(sample_any_kernel, dim3(a.B), dim3(kAnyThreads), 0, st, a);
     return;
   }
-  const int pw = ((a.V + C * kSampThreads - 1) / (C * kSampThreads)) * 32;
+  const int pw = ((a.V + C * kSW * 32 * kU - 1) / (C * kSW * 32 * kU)) * 32 * kU;
   launch_k_cluster(sample_kernel, dim3(C * a.B), dim3(kSampThreads),
                    sample_smem(C, kSW * pw), st, C, a, C, pw);
 }
