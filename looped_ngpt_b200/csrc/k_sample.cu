@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   float minp = a.min_p ? a.min_p[row] : 0.f, topp = a.top_p ? a.top_p[row] : 1.f;
   minp = minp > 0.f ? fminf(minp, 1.f) : 0.f;
   const float uf = a.uniform[row];
+  const bool cuts = k < a.V || topp < 1.f;
 
   // ---- the slice, its largest and smallest finite logit ---------------------
   // In four parts, so that the first are looked at while the others arrive: a
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   float vmax = -INFINITY, vmin = INFINITY;          // of what may be drawn
   auto look = [&](float v) {
     vmax = fmaxf(vmax, v);                          // (passes over NaN)
-    if (k < a.V && v > -INFINITY) vmin = fminf(vmin, v);
+    if (cuts && v > -INFINITY) vmin = fminf(vmin, v);
   };
   if (tid < head) look(src[tid]);
   if (tid < cnt - tail) look(src[tail + tid]);
@@ -256,8 +257,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     }
     return;
   }
-  // lo: the smallest logit where a top-k may need it, else -inf
-  float m = key_float(kmax), lo = k < a.V ? fminf(m, key_float(kmin)) : -INFINITY;
+  // lo: the smallest logit where a cutoff is looked for, else -inf
+  float m = key_float(kmax), lo = cuts ? fminf(m, key_float(kmin)) : -INFINITY;
   if (greedy) {
     // the lowest index of the largest logit, in the first block that has it
     const unsigned has = __ballot_sync(0xffffffffu, lane < C && s.ex.max[lane] == kmax);
@@ -360,10 +361,25 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       const bool f32 = span > 1e-30f && span < 1e30f;
       const float sf = f32 ? (float)kNB / span : 0.f;
       const double hd = (double)hi, sc = low == hi ? 0.0 : (double)kNB / (hd - (double)low);
+      auto bins_of = [&](auto& q, const auto& v) {      // for v <= hi
+        constexpr int N = sizeof(v) / sizeof(v[0]);
+        if (f32) {
+#pragma unroll
+          for (int u = 0; u < N; ++u)
+            q[u] = __float_as_int(fmaf(hi - v[u], sf, 0x1.8p23f - 0.5f)) - 0x4b400000;
+        } else {
+#pragma unroll
+          for (int u = 0; u < N; ++u)
+            q[u] = __double2loint(fma(hd - (double)v[u], sc, 0x1.8p52 - 0.5));
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u) q[u] = min(q[u], kNB - 1);
+      };
       auto bin_of = [&](float v) {
-        const int q = f32 ? __float_as_int(fmaf(hi - v, sf, 0x1.8p23f - 0.5f)) - 0x4b400000
-                          : __double2loint(fma(hd - (double)v, sc, 0x1.8p52 - 0.5));
-        return max(0, min(q, kNB - 1));
+        const float one[1] = {v};
+        int q[1];
+        bins_of(q, one);
+        return q[0];
       };
       __syncthreads();
       for (int i = tid; i < kHistWords; i += kSampThreads) hist_all[i] = 0;
@@ -375,37 +391,32 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       __syncthreads();
       uint32_t* hist = hist_all + w * 2 * kNB;
       auto count = [&](int bn, u64 f) {
-        const uint32_t f0 = (uint32_t)f & 0x3fffffu, f1 = (uint32_t)(f >> 22);
-        if (f0) atomicAdd(hist + bn, f0);
-        if (f1) atomicAdd(hist + kNB + bn, f1);
+        atomicAdd(hist + bn, (uint32_t)f & 0x3fffffu);
+        if (by_mass) atomicAdd(hist + kNB + bn, (uint32_t)(f >> 22));
       };
       if (level == 0) {
         for (int q = 0; q < run; q += kU) {
           float v[kU];
-          uint32_t in = 0;
+          bool in[kU], any = false;
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
             const int i = i0 + 32 * (q + u);
             v[u] = zs[i];
-            in |= (uint32_t)(v[u] >= low) << u;
-            if (cut && v[u] <= cz && !(v[u] == cz && base + i <= ci)) in &= ~(1u << u);
+            in[u] = v[u] >= low;
+            if (cut && v[u] <= cz && !(v[u] == cz && base + i <= ci)) in[u] = false;
+            any |= in[u];
           }
           uint32_t word = 0xffffffffu;
-          if (__any_sync(0xffffffffu, in)) {
+          if (__any_sync(0xffffffffu, any)) {
             int bn[kU];
-            u64 f[kU];
             double x[kU];
             if (by_mass) weights(x, v);
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-              bn[u] = bin_of(v[u]);
-              f[u] = by_mass ? as_fixed(x[u]) : 1;
-            }
+            bins_of(bn, v);
 #pragma unroll
             for (int u = 0; u < kU; ++u)
-              if (in >> u & 1) {
-                word ^= (bn[u] ^ 255) << (8 * u);
-                count(bn[u], f[u]);
+              if (in[u]) {
+                word = __byte_perm(word, bn[u], 0x3210 + ((4 - u) << (4 * u)));
+                count(bn[u], by_mass ? as_fixed(x[u]) : 1);
               }
           }
           bins[(q / kU) * kSampThreads] = word;
@@ -752,7 +763,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     double x[kU];
     weights(x, v);                     // (of anything where `in` is false)
 #pragma unroll
-    for (int u = 0; u < kU; ++u) sum += in[u] ? x[u] : 0.0;
+    for (int u = 0; u < kU; ++u)
+      if (in[u]) sum += x[u];
   }
   sum = wsum(sum);
   if (lane == 0) s.dred[w] = sum;
