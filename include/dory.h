@@ -337,8 +337,12 @@ int dory_decode_step_mixed(dory_model* m, dory_cache* c,
  * order (z descending, index ascending) and never none; the token is the
  * first kept one in index order whose running sum of w exceeds u times the
  * kept sum (u outside [0, 1) is clamped; the last kept token for u = 1).
- * Weights and sums are f64.  A -inf or NaN logit is never drawn; tokens at
- * +inf share the row equally; a row with nothing to draw gets token -1 and
+ * Sums are f64, weights f64 with a relative error below 2^-38, and top-p
+ * compares them as integers of 43 bits (V up to 262144; above, one block per
+ * row works in f64 throughout, and is slow): a uniform, or a share, that lies
+ * closer to a border than that may fall to its other side.  Tokens below
+ * e^-44 of the largest weight are not drawn, nor is a -inf or NaN logit;
+ * tokens at +inf share the row equally; a row with nothing to draw gets token -1 and
  * log-probability -inf.  d_tokens int32 [B]; d_logprobs f32 [B] or NULL: the
  * log-probability of the token in the distribution it was drawn from.
  * Needs no workspace and allocates nothing.  Enqueued on `stream`.  Errors:
@@ -364,7 +368,16 @@ typedef struct {
   const int32_t* block_table; /* [batch][pages_per_seq]                      */
   int n_pages, pages_per_seq, batch, n_kv_heads;
   int head_dim;               /* 64, 128 or 160                              */
+  const void* plan;           /* from dory_kv8_plan, or NULL                 */
 } dory_kv8;
+
+/* Write the launch plan of a cache (the TMA maps of its pages) to
+ * DORY_KV8_PLAN_BYTES of 64-byte aligned host memory, to be set as `plan`:
+ * it saves dory_kv8_attend building it in every call.  It holds for these k,
+ * v, n_pages, n_kv_heads and head_dim.  Errors: DORY_ERR_ARG,
+ * DORY_ERR_UNSUPPORTED, DORY_ERR_CUDA. */
+#define DORY_KV8_PLAN_BYTES 512
+int dory_kv8_plan(const dory_kv8* c, void* plan);
 
 /* Append K/V rows (bf16 [batch][T][n_kv_heads][head_dim]; *_strides: host
  * arrays of the element strides of sequence, token and head, multiples of

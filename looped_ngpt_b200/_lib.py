@@ -16,6 +16,7 @@ ERRORS = {-1: "DORY_ERR_ARG", -2: "DORY_ERR_UNSUPPORTED", -3: "DORY_ERR_CACHE",
           -4: "DORY_ERR_CUDA", -5: "DORY_ERR_TIMEOUT", -6: "DORY_ERR_WORKSPACE",
           -7: "DORY_ERR_DEVICE"}
 KV_MODES = {"per_loop": 0, "last_loop": 1}
+KV8_PLAN_BYTES = 512
 KV_FMTS = {"bf16": 0, "e4m3": 1}
 
 
@@ -36,7 +37,8 @@ class DoryKv8(Structure):
     _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p),
                 ("v_scale", c_void_p), ("block_table", c_void_p),
                 ("n_pages", c_int), ("pages_per_seq", c_int),
-                ("batch", c_int), ("n_kv_heads", c_int), ("head_dim", c_int)]
+                ("batch", c_int), ("n_kv_heads", c_int), ("head_dim", c_int),
+                ("plan", c_void_p)]
 
 
 class DoryKernelStat(Structure):
@@ -86,6 +88,7 @@ SIGNATURES = {
                             _P, _P]),
     "dory_kv8_append": (c_int, [POINTER(DoryKv8), _P, _P, _I64P, _I64P, c_int,
                                 _P, _P, _P]),
+    "dory_kv8_plan": (c_int, [POINTER(DoryKv8), _P]),
     "dory_kv8_workspace_bytes": (c_int, [POINTER(DoryKv8), c_int, _I64P]),
     "dory_kv8_attend": (c_int, [POINTER(DoryKv8), _P, _I64P, c_int, _P, c_int,
                                 ctypes.c_float, _P, _P, c_int64, _P]),

@@ -748,23 +748,25 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   const float from = fmaxf(cz, floor);
   auto kept = [&](float v, int i) { return v >= from && (v > cz || (v == cz && base + i <= ci)); };
   double sum = 0.0;
-  for (int q = 0; q < run; q += kU) {
-    float v[kU];
-    bool in[kU], any = false;
+  uint32_t mask = 0;                   // this thread's kept logits
+  if (cut) {
+#pragma unroll 4
+    for (int q = 0; q < run; ++q) mask |= (uint32_t)kept(zs[i0 + 32 * q], i0 + 32 * q) << q;
+  }
+  if (cut && 3 * (int)__reduce_max_sync(0xffffffffu, (unsigned)__popc(mask)) < run) {
+    // few: each by itself (P = 0.9 of 64 x 131072: 54 -> 51 us)
+    for (uint32_t r = mask; r; r &= r - 1) sum += weight(zs[i0 + 32 * (__ffs(r) - 1)]);
+  } else {
+    for (int q = 0; q < run; q += kU) {
+      float v[kU];
+      double x[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int i = i0 + 32 * (q + u);
-      v[u] = zs[i];
-      in[u] = v[u] >= from;
-      if (cut && v[u] == cz && base + i > ci) in[u] = false;
-      any |= in[u];
+      for (int u = 0; u < kU; ++u) v[u] = zs[i0 + 32 * (q + u)];
+      weights(x, v);                   // (of anything that is not kept)
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (cut ? mask >> (q + u) & 1 : v[u] >= from) sum += x[u];
     }
-    if (!__any_sync(0xffffffffu, any)) continue;
-    double x[kU];
-    weights(x, v);                     // (of anything where `in` is false)
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-      if (in[u]) sum += x[u];
   }
   sum = wsum(sum);
   if (lane == 0) s.dred[w] = sum;

@@ -28,6 +28,7 @@ int check_kv8(const dory_kv8* c) {
     return DORY_ERR_UNSUPPORTED;
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 160)
     return DORY_ERR_UNSUPPORTED;
+  if (!aligned(c->plan, 64)) return DORY_ERR_ARG;
   return DORY_OK;
 }
 
@@ -83,6 +84,16 @@ int dory_kv8_append(const dory_kv8* c, const void* d_k, const void* d_v,
   return launched();
 }
 
+static_assert(sizeof(Kv8Maps) <= DORY_KV8_PLAN_BYTES, "the plan holds the maps");
+
+int dory_kv8_plan(const dory_kv8* c, void* plan) {
+  const int rc = check_kv8(c);
+  if (rc) return rc;
+  if (!plan || !aligned(plan, 64)) return DORY_ERR_ARG;
+  if ((int64_t)c->n_pages * c->n_kv_heads * kPage > INT_MAX) return DORY_ERR_UNSUPPORTED;
+  return make_kv8_maps(to_kv8(c), (Kv8Maps*)plan) ? DORY_OK : DORY_ERR_CUDA;
+}
+
 int dory_kv8_workspace_bytes(const dory_kv8* c, int n_q_heads, int64_t* bytes) {
   const int rc = check_kv8(c);
   if (rc) return rc;
@@ -113,11 +124,11 @@ int dory_kv8_attend(const dory_kv8* c, const void* d_q,
   cudaGetLastError();
   int* err = device_status_word();
   Kv8Maps maps;
-  if (!err || !make_kv8_maps(to_kv8(c), &maps)) return DORY_ERR_CUDA;
+  if (!err || (!c->plan && !make_kv8_maps(to_kv8(c), &maps))) return DORY_ERR_CUDA;
   launch_kv8_attend(Kv8AttendArgs{to_kv8(c), c->batch, n_q_heads / c->n_kv_heads,
                                   (const bf16*)d_q, q_strides[0], q_strides[1], d_len, window,
                                   scale, (bf16*)d_out, d_ws, err, nullptr},
-                    maps, (cudaStream_t)stream);
+                    c->plan ? *(const Kv8Maps*)c->plan : maps, (cudaStream_t)stream);
   return launched();
 }
 

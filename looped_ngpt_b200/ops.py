@@ -54,31 +54,34 @@ def _cuda(t, name):
     return t.device
 
 
-class _On:
-    """The device made current and the stream work goes to; outputs allocated
-    inside belong to that stream."""
+def _here(device):
+    """The device's current stream if the device is the current one, else
+    None (then work is enqueued inside _On)."""
+    if torch.cuda.current_device() == device.index:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
 
-    __slots__ = ("stream", "ctx")
+
+class _On:
+    """The device made current, and `stream` (None: the device's current one),
+    so that outputs allocated inside belong to the stream the work goes to."""
 
     def __init__(self, device, stream):
         if stream is None:
-            self.stream = torch._C._cuda_getCurrentRawStream(device.index)
-            self.ctx = (None if torch.cuda.current_device() == device.index
-                        else torch.cuda.device(device))
+            self.ctx = torch.cuda.device(device)
+        elif stream.device != device:
+            raise ValueError(f"stream: on {stream.device}, the tensors are on "
+                             f"{device}")
         else:
-            if stream.device != device:
-                raise ValueError(f"stream: on {stream.device}, the tensors are "
-                                 f"on {device}")
-            self.stream, self.ctx = stream.cuda_stream, torch.cuda.stream(stream)
+            self.ctx = torch.cuda.stream(stream)
+        self.device = device
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.stream
+        self.ctx.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
 
 
 def sample(logits, uniform, temperature=None, top_k=None, top_p=None,
@@ -116,15 +119,24 @@ def sample(logits, uniform, temperature=None, top_k=None, top_p=None,
     lp = None
     if logprobs is not False and logprobs is not True:
         lp = _dense(logprobs, "logprobs", _F32, row, dev)
-    with _On(dev, stream) as st:
+
+    def enqueue(st, tokens, lp):
         if tokens is None:
             tokens = torch.empty_like(uniform, dtype=_I32)
         if logprobs is True:
             lp = torch.empty_like(uniform)
-        check("dory_sample", _lib.load().dory_sample(
+        rc = _lib.load().dory_sample(
             logits.data_ptr(), ld, B, V, T, k, p, m, uniform.data_ptr(),
-            tokens.data_ptr(), None if lp is None else lp.data_ptr(), st))
-    return tokens, lp
+            tokens.data_ptr(), None if lp is None else lp.data_ptr(), st)
+        if rc:
+            check("dory_sample", rc)
+        return tokens, lp
+
+    st = _here(dev) if stream is None else None
+    if st is not None:
+        return enqueue(st, tokens, lp)
+    with _On(dev, stream) as st:
+        return enqueue(st, tokens, lp)
 
 
 class KV8Pages:
@@ -162,6 +174,11 @@ class KV8Pages:
                          v_scale.data_ptr(), block_table.data_ptr(), shape[0],
                          self.pages_per_seq, self.batch, shape[1], shape[3])
         self._ref = ctypes.byref(self.c)
+        # the TMA maps of the pages, built once
+        self._plan = ctypes.create_string_buffer(_lib.KV8_PLAN_BYTES + 64)
+        plan = -(-ctypes.addressof(self._plan) // 64) * 64
+        check("dory_kv8_plan", _lib.load().dory_kv8_plan(self._ref, plan))
+        self.c.plan = plan
         self._ws = {}
         self._rows = self._q_rows = (None,)
         self._q_heads = [g * shape[1] for g in (1, 2, 4, 8)]
@@ -208,9 +225,15 @@ class KV8Pages:
             self._rows = (key, _I64x3(*_rows(k, "k", 3)),
                           _I64x3(*_rows(v, "v", 3)))
         _, ks, vs = self._rows
-        with _On(dev, stream) as st:
-            check("dory_kv8_append", _lib.load().dory_kv8_append(
-                self._ref, pk, pv, ks, vs, T, pos.data_ptr(), n, st))
+        args = (self._ref, pk, pv, ks, vs, T, pos.data_ptr(), n)
+        st = _here(dev) if stream is None else None
+        if st is not None:
+            rc = _lib.load().dory_kv8_append(*args, st)
+        else:
+            with _On(dev, stream) as st:
+                rc = _lib.load().dory_kv8_append(*args, st)
+        if rc:
+            check("dory_kv8_append", rc)
 
     def workspace(self, n_q_heads):
         """A workspace for attend with n_q_heads query heads; one
@@ -228,7 +251,8 @@ class KV8Pages:
         head_dim], over the lens[b] (int32 [batch]) cached tokens, the last
         `window` of them if window > 0; scale defaults to 1 / sqrt(head_dim).
         Returns bf16 [batch, n_q_heads, head_dim] (`out`, if given).  Without
-        `ws` one workspace per stream is kept by this object."""
+        `ws` this object keeps one workspace per stream, and a captured graph
+        gets one of its own."""
         dev, B, hd = self.device, self.batch, self.head_dim
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q: bf16 [batch, n_q_heads, head_dim] is needed")
@@ -247,16 +271,28 @@ class KV8Pages:
             self._q_rows = (key, _I64x2(*_rows(q, "q", 2)))
         if out is not None:
             _dense(out, "out", _BF16, shape, dev)
+        if scale is None:
+            scale = hd ** -0.5
+        st = _here(dev) if stream is None else None
+        if st is not None:
+            return self._attend(st, pq, q, lens, window, scale, out, ws)
         with _On(dev, stream) as st:
-            if out is None:
-                out = (torch.empty_like(q) if q.is_contiguous()
-                       else torch.empty(shape, dtype=_BF16, device=dev))
+            return self._attend(st, pq, q, lens, window, scale, out, ws)
+
+    def _attend(self, st, pq, q, lens, window, scale, out, ws):
+        Hq = q.shape[1]
+        if out is None:
+            out = (torch.empty_like(q) if q.is_contiguous()
+                   else torch.empty(q.shape, dtype=_BF16, device=self.device))
+        if ws is None and torch.cuda.is_current_stream_capturing():
+            ws = self.workspace(Hq)          # the graph's own
+        elif ws is None:
+            ws = self._ws.get((st, Hq))
             if ws is None:
-                ws = self._ws.get((st, Hq))
-                if ws is None:
-                    ws = self._ws[st, Hq] = self.workspace(Hq)
-            check("dory_kv8_attend", _lib.load().dory_kv8_attend(
-                self._ref, pq, self._q_rows[1], Hq, lens.data_ptr(), window,
-                hd ** -0.5 if scale is None else scale, out.data_ptr(),
-                ws.data_ptr(), ws.numel(), st))
+                ws = self._ws[st, Hq] = self.workspace(Hq)
+        rc = _lib.load().dory_kv8_attend(
+            self._ref, pq, self._q_rows[1], Hq, lens.data_ptr(), window, scale,
+            out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+        if rc:
+            check("dory_kv8_attend", rc)
         return out

@@ -37,7 +37,7 @@ def test_sample_refusals():
     (dict(k=P + 8), -1), (dict(v_scale=P + 4), -1), (dict(n_pages=0), -1),
     (dict(batch=0), -1), (dict(pages_per_seq=0), -1), (dict(n_kv_heads=0), -1),
     (dict(head_dim=96), -2), (dict(pages_per_seq=1 << 26), -2),
-    (dict(batch=70000), -2),
+    (dict(batch=70000), -2), (dict(plan=P + 8), -1),
 ])
 def test_kv8_refuses_a_bad_cache(over, code):
     lib = _lib.load()
@@ -45,6 +45,7 @@ def test_kv8_refuses_a_bad_cache(over, code):
     n = ctypes.c_int64()
     assert lib.dory_kv8_append(c, P, P, S3, S3, 1, P, None, None) == code
     assert lib.dory_kv8_workspace_bytes(c, 16, ctypes.byref(n)) == code
+    assert lib.dory_kv8_plan(c, P) == code
     assert lib.dory_kv8_attend(c, P, S2, 16, P, 0, 1.0, P, P, 1 << 30, None) == code
 
 
@@ -79,6 +80,15 @@ def test_kv8_attend_refusals():
     assert f(c, P, S2, 18, P, 0, 1.0, P, P, big, None) == -1    # 18 on 4 heads
     assert f(c, P, S2, 12, P, 0, 1.0, P, P, big, None) == -2    # 3 per head
     assert f(c, P, S2, 64, P, 0, 1.0, P, P, big, None) == -2    # 16 per head
+
+
+def test_kv8_plan_refusals():
+    f = _lib.load().dory_kv8_plan
+    assert f(None, P) == -1
+    assert f(ctypes.byref(_kv8()), None) == -1
+    assert f(ctypes.byref(_kv8()), P + 32) == -1
+    # 2^31 rows and more
+    assert f(ctypes.byref(_kv8(n_pages=1 << 25, n_kv_heads=1)), P) == -2
 
 
 def test_python_refuses_what_is_not_on_a_gpu():
