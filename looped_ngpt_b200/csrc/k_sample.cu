@@ -344,8 +344,127 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     lo = fmaxf(lo, cz);
   }
 
-  // ---- one cutoff: by count (top-k) or by mass (top-p) ----------------------
-  auto select = [&](const bool by_mass) {
+  // ---- few logits: the row's blocks send each other those in their masks (at
+  // `to`; s.n is 0), which hold the top k, and decide from the list; false if
+  // a block has too many to send.  Block 0 then finishes the row.
+  auto listed = [&](uint32_t mask, Cand* to) -> bool {
+    const int mine = __popc(mask), warps = __reduce_add_sync(0xffffffffu, mine);
+    if (warps) {
+      int at = 0, inc = mine;
+      if (lane == 0) at = atomicAdd(&s.n, warps);
+      at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      at += inc - mine;
+      for (uint32_t r = mask; r; r &= r - 1, ++at) {
+        const int i = i0 + 32 * (__ffs(r) - 1);
+        const float v = zs[i];
+        const double x = v >= floor ? weight(fmaxf(v, floor)) : 0.0;
+        if (at < gc) own_cand[at] = Cand{v, base + i, (u64)__double_as_longlong(x)};
+      }
+    }
+    __syncthreads();
+    const int own = s.n, send = own <= gc ? own : 0;
+    if (tid < C) put32(&s.ex.l_n[rank], tid, own);
+    for (int i = tid; i < C * send; i += kSampThreads) {
+      const int c = i / send, j = i - c * send;
+      const Cand x = own_cand[j];
+      Cand* there = to + rank * gc + j;
+      put32(&there->z, c, __float_as_uint(x.z));
+      put32(&there->i, c, x.i);
+      put64(&there->w, c, x.w);
+    }
+    cluster_sync_all();
+    const int ln = lane < C ? s.ex.l_n[lane] : 0;
+    const int n = __reduce_add_sync(0xffffffffu, ln);
+    if (n > kRank || !__all_sync(0xffffffffu, ln <= gc)) return false;
+    if (rank) return true;
+    Cand* list = own_cand;                          // as they came
+    Cand* by_index = list + kRank;
+    double* kw = reinterpret_cast<double*>(by_index + kRank);
+    for (int e = tid; e < C * gc; e += kSampThreads) {
+      const int c = e / gc, j = e - c * gc;
+      if (j < s.ex.l_n[c]) {
+        int at = j;
+        for (int q = 0; q < c; ++q) at += s.ex.l_n[q];
+        list[at] = to[e];
+      }
+    }
+    __syncthreads();
+    if (tid < n) {
+      // its place by index, and by (z, index): beyond k it weighs nothing
+      Cand me = list[tid];
+      int at = 0, before = 0;
+#pragma unroll 4
+      for (int q = 0; q < n; ++q) {
+        const Cand o = list[q];
+        at += o.i < me.i;
+        before += o.z > me.z || (o.z == me.z && o.i < me.i);
+      }
+      if (before >= k) me.w = 0;                    // (+0.0)
+      by_index[at] = me;
+    }
+    __syncthreads();
+    if (tid < n) {
+      // mass before it by (z, index), and of all
+      const Cand me = by_index[tid];
+      double before = 0.0, all = 0.0;
+      bool first = true;
+#pragma unroll 4
+      for (int q = 0; q < n; ++q) {
+        const Cand o = by_index[q];
+        const double x = __longlong_as_double((long long)o.w);
+        const bool b = o.z > me.z || (o.z == me.z && q < tid);
+        all += x;
+        before += b ? x : 0.0;
+        first = first && !b;
+      }
+      const bool in = !(topp < 1.f) || first || before < (double)topp * all;
+      kw[tid] = in ? __longlong_as_double((long long)me.w) : 0.0;
+    }
+    __syncthreads();
+    if (w) return true;
+    // running mass in index order, four neighbours per lane
+    double x[kRank / 32], sum = 0.0;
+#pragma unroll
+    for (int u = 0; u < kRank / 32; ++u) {
+      const int e = kRank / 32 * lane + u;
+      x[u] = e < n ? kw[e] : 0.0;
+      sum += x[u];
+    }
+    double inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const double total = __shfl_sync(0xffffffffu, inc, 31);
+    const double target = (uf > 0.f ? fmin((double)uf, 1.0) : 0.0) * total;
+    const unsigned any = __ballot_sync(0xffffffffu, sum > 0.0);
+    const unsigned hit = __ballot_sync(0xffffffffu, sum > 0.0 && inc > target);
+    if (lane == (hit ? __ffs(hit) - 1 : 31 - __clz(any))) {
+      double c = inc - sum;
+      int pick = -1;
+#pragma unroll
+      for (int u = 0; u < kRank / 32; ++u)
+        if (x[u] > 0.0 && (pick < 0 || !(c > target))) {
+          pick = kRank / 32 * lane + u;
+          c += x[u];
+        }
+      const Cand me = by_index[pick];
+      a.tokens[row] = me.i;
+      if (a.logprobs)
+        a.logprobs[row] = (float)((me.z == m ? 0.0 : ((double)me.z - md) * inv_t) - log(total));
+    }
+    return true;
+  };
+
+  // ---- one cutoff: by count (top-k) or by mass (top-p); true if the row is
+  // finished --------------------------------------------------------------------
+  auto select = [&](const bool by_mass) -> bool {
     float hi = m, low = lo;
     // below m - 31 T integer weights are 0
     if (by_mass) low = fmaxf(fmaxf(low, m - 31.f * T), -FLT_MAX);
@@ -479,10 +598,22 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       const int bin = s.bin;
       if (bin < 0) {
         cluster_sync_all();             // the histograms have been read
-        return;
+        return false;
       }
       mass_above = s.mass_above;
       want = s.want;
+      if (!by_mass && level == 0 && mass_above + s.bin_mass[bin] <= (u64)kRank) {
+        // all logits down to the bin's end are few
+        uint32_t upto = 0;
+        for (int q = 0; q < run; q += kU) {
+          const uint32_t e = __vcmpleu4(bins[(q / kU) * kSampThreads], bin * 0x01010101u) & 0x08040201u;
+          upto |= ((e | e >> 8 | e >> 16 | e >> 24) & 15u) << q;
+        }
+        if (listed(upto, ex_cand)) return true;
+        __syncthreads();
+        if (tid == 0) s.n = 0;
+        __syncthreads();
+      }
       // the bin's logits
       if (level == 0) {
         for (int q = 0; q < run; q += kU) {
@@ -581,7 +712,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
         __syncthreads();
         cz = s.cut_z;
         ci = s.cut_i;
-        return;
+        return false;
       }
       if (low == hi) {
         // equal logits: the r-th of them in index order
@@ -608,16 +739,16 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
         cluster_sync_all();
         cz = low;
         ci = s.ex.tie;
-        return;
+        return false;
       }
     }
   };
   if (k < a.V) {
-    select(false);
+    if (select(false)) return;
     cut = true;
     lo = fmaxf(lo, cz);
   }
-  // ---- few kept: every block gets them all, and decides without the rest -----
+  // few kept, and not listed yet (the histogram's bin held too many)
   if (k <= kRank) {
     uint32_t mask = 0;
     for (int q = 0; q < run; ++q) {
@@ -628,115 +759,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     __syncthreads();
     if (tid == 0) s.n = 0;
     __syncthreads();
-    const int mine = __popc(mask), warps = __reduce_add_sync(0xffffffffu, mine);
-    int at = 0;
-    if (warps) {
-      if (lane == 0) at = atomicAdd(&s.n, warps);
-      at = __shfl_sync(0xffffffffu, at, 0);
-      int inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      at += inc - mine;
-      for (uint32_t r = mask; r; r &= r - 1, ++at) {
-        const int i = i0 + 32 * (__ffs(r) - 1);
-        if (at < gc) own_cand[at] = Cand{zs[i], base + i, (u64)__double_as_longlong(weight(zs[i]))};
-      }
-    }
-    __syncthreads();
-    const int own = s.n, send = own <= gc ? own : 0;
-    Cand* ex_list = reinterpret_cast<Cand*>(bins - tid);
-    if (tid < C) put32(&s.ex.l_n[rank], tid, own);
-    for (int i = tid; i < C * send; i += kSampThreads) {
-      const int c = i / send, j = i - c * send;
-      const Cand x = own_cand[j];
-      Cand* to = ex_list + rank * gc + j;
-      put32(&to->z, c, __float_as_uint(x.z));
-      put32(&to->i, c, x.i);
-      put64(&to->w, c, x.w);
-    }
-    cluster_sync_all();
-    const int ln = lane < C ? s.ex.l_n[lane] : 0;
-    const int n = __reduce_add_sync(0xffffffffu, ln);
-    if (n <= kRank && __all_sync(0xffffffffu, ln <= gc)) {
-      if (rank) return;
-      Cand* list = own_cand;                          // as they came
-      Cand* by_index = list + kRank;
-      double* kw = reinterpret_cast<double*>(by_index + kRank);
-      for (int e = tid; e < C * gc; e += kSampThreads) {
-        const int c = e / gc, j = e - c * gc;
-        if (j < s.ex.l_n[c]) {
-          int to = j;
-          for (int q = 0; q < c; ++q) to += s.ex.l_n[q];
-          list[to] = ex_list[e];
-        }
-      }
-      __syncthreads();
-      if (tid < n) {
-        const Cand me = list[tid];
-        int to = 0;
-#pragma unroll 4
-        for (int q = 0; q < n; ++q) to += list[q].i < me.i;
-        by_index[to] = me;
-      }
-      __syncthreads();
-      if (tid < n) {
-        // mass before it by (z, index), and of all
-        const Cand me = by_index[tid];
-        double before = 0.0, all = 0.0;
-        bool first = true;
-#pragma unroll 4
-        for (int q = 0; q < n; ++q) {
-          const Cand o = by_index[q];
-          const double x = __longlong_as_double((long long)o.w);
-          const bool b = o.z > me.z || (o.z == me.z && q < tid);
-          all += x;
-          before += b ? x : 0.0;
-          first = first && !b;
-        }
-        const bool in = !(topp < 1.f) || first || before < (double)topp * all;
-        kw[tid] = in ? __longlong_as_double((long long)me.w) : 0.0;
-      }
-      __syncthreads();
-      if (w == 0) {
-        // running mass in index order, four neighbours per lane
-        double x[kRank / 32], sum = 0.0;
-#pragma unroll
-        for (int u = 0; u < kRank / 32; ++u) {
-          const int e = kRank / 32 * lane + u;
-          x[u] = e < n ? kw[e] : 0.0;
-          sum += x[u];
-        }
-        double inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
-        }
-        const double total = __shfl_sync(0xffffffffu, inc, 31);
-        const double target = (uf > 0.f ? fmin((double)uf, 1.0) : 0.0) * total;
-        const unsigned any = __ballot_sync(0xffffffffu, sum > 0.0);
-        const unsigned hit = __ballot_sync(0xffffffffu, sum > 0.0 && inc > target);
-        if (lane == (hit ? __ffs(hit) - 1 : 31 - __clz(any))) {
-          double c = inc - sum;
-          int pick = -1;
-#pragma unroll
-          for (int u = 0; u < kRank / 32; ++u)
-            if (x[u] > 0.0 && (pick < 0 || !(c > target))) {
-              pick = kRank / 32 * lane + u;
-              c += x[u];
-            }
-          const Cand me = by_index[pick];
-          a.tokens[row] = me.i;
-          if (a.logprobs)
-            a.logprobs[row] =
-                (float)((me.z == m ? 0.0 : ((double)me.z - md) * inv_t) - log(total));
-        }
-      }
-      return;
-    }
+    // (the bins have been read by now)
+    if (listed(mask, reinterpret_cast<Cand*>(bins - tid))) return;
   }
   if (topp < 1.f) {
     select(true);
