@@ -28,7 +28,10 @@ namespace {
 // spent on 8 elements: 8 row groups x one 16-byte chunk per thread, so that a
 // thread's four chunks are 8 rows apart; magnitudes are compared as packed
 // 16-bit integers, and again without infinities and NaN only where there are
-// some.  The rows are asked for before the page number has arrived.
+// some.  The rows are asked for before the page number has arrived.  24 x up
+// to 2048 rows of 8 heads x 128 (151 MB): 29 us, 80% of the copy rate (with 8
+// elements per thread in order, f32 comparisons and the rows behind the page
+// number: 37 us); 8192 rows of 4 x 160 6.7 us (floor 4.8); one row 1.9 us.
 template <int HD, bool PAGED>
 __global__ void __launch_bounds__(HD) kv8_append_kernel(Kv8AppendArgs a) {
   constexpr int CH = HD / 8, NT = HD;          // 16-byte chunks per row; threads

@@ -36,6 +36,12 @@
 // loads of K and the transposing ldmatrix of V are free of conflicts.  (One
 // TMA instruction per tile: the same blocks as 16 bulk copies of 4 rows cost
 // 160 issue slots per block, a third of the kernel's instructions.)
+//
+// Times (head_dim 160, 4 query heads per KV head, 4 KV heads, of 6.55 TB/s):
+// 64 sequences of 32768 tokens 414 us (99%), 4 of 131072 114 us (90%), one of
+// 2048 8.2 us, a chain of lengths -> page -> tile -> product -> join.  48 sequences of up
+// to 9001 tokens behind a 1024-token window (head_dim 128, 8 x 8 heads) take
+// 32 us (46%): 10 blocks per warp do not amortise that chain.
 #include <algorithm>
 
 #include "async_copy.cuh"

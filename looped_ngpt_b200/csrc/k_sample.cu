@@ -19,9 +19,21 @@
 // same decision from the same values.  A cutoff (top-k by count, top-p by
 // mass) is found by histograms of kNB linear bins over the range of the
 // logits still in question, narrowed until the bin that holds it has at most
-// kGC logits per block (or equal ones), which are then ranked exactly: two
-// exchanges per level, one or two levels unless the logits are adversarial.
-// Rows without cutoffs need one exchange.
+// kRank logits (or equal ones), which are then ranked exactly: two exchanges
+// per level, one or two levels unless the logits are adversarial.  A top-k
+// that leaves up to kRank logits is finished from one list of them.  Rows
+// without cutoffs need two exchanges.
+//
+// Reading 64 x 131072 logits takes 5.1 us at the copy rate.  The kernel takes
+// 28 us without cutoffs, 51 us with top-p 0.9 and 37 us with top-k 50 and
+// top-p 0.95 (13.5 us for one such row): two waves of eight-block clusters
+// (64 KB of logits and 45 KB of exchange per block, two blocks per SM), each
+// a chain of exchanges of 0.7 us and, per logit, 60 instructions in all
+// without cutoffs and 115 with a top-p; issue slots are 55% busy, the f64 pipe
+// 11 to 20%.  Measured and not kept: 16-block clusters of 8192 logits for many
+// rows (40 / 95 us where 8-block ones took 28.5 / 58), 256 threads with 128
+// registers (30 / 60 against the same), one copy of the cutoff code for both
+// kinds (29 / 55 against 28 / 51).
 #include "async_copy.cuh"
 #include "common.cuh"
 
