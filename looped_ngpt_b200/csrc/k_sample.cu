@@ -69,23 +69,29 @@ __constant__ double kExpTab[16] = {
     0x1.6a09e667f3bcdp+0, 0x1.7a11473eb0187p+0, 0x1.8ace5422aa0dbp+0, 0x1.9c49182a3f090p+0,
     0x1.ae89f995ad3adp+0, 0x1.c199bdd85529cp+0, 0x1.d5818dcfba487p+0, 0x1.ea4afa2a490dap+0};
 
-// 2^(y/16) for -1100 < y <= 0 (1 at 0), relative error below 2^-38: y = 16 n +
-// j + f, |f| <= 1/2, by 2^n 2^(j/16) and the polynomial of degree 4 through 1
-// at 0 whose largest relative error over |f| <= 1/2 is least (2.5e-12; fitted
-// by reweighted least squares).  tab: 2^(j/16) in shared memory (16 doubles,
-// one per bank pair).  An error of 2^-38 in the weights moves the borders of a
-// row's running sum so little that a uniform falls between with a chance
-// below 1e-6 at V = 131072, while sampling is bound by these f64 operations.
-__device__ __forceinline__ double exp2_16th(double y, const double* tab) {
-  constexpr double kMagic = 0x1.8p52;
-  const double t = y + kMagic, f = y - (t - kMagic);
-  const int k = __double2loint(t);
-  double p = fma(f, 0x1.3b29bf8ba0f3ap-23, 0x1.c6b3f5b3946b2p-17);
-  p = fma(p, f, 0x1.ebfbdfff31574p-11);
-  p = fma(p, f, 0x1.62e42fec3f16fp-5);
+// 2^(y/16) for -1100 < y <= 0 (1 at 0) as p s, relative error below 2^-36.9: y
+// = 16 n + j + f, |f| <= 1/2, with s = 2^n 2^(j/16) and p the polynomial of
+// degree 4 through 1 at 0 whose largest relative error over |f| <= 1/2 is least
+// (2^-38.5; fitted by reweighted least squares).  y is rounded to 2^-32 (2^-37.5
+// of the weight) by adding 1.5 2^20 + 1/2, which leaves 16 n + j in the upper
+// word and f + 1/2 in the lower.  tab: 2^(j/16), its upper word less j << 16,
+// in shared memory (16 doubles, one per bank pair).  Errors of 2^-36.9 in the
+// weights move the borders of a row's running sum so little that a uniform falls
+// between with a chance below 1e-6 at V = 131072, while sampling is bound by
+// the instructions of these lines.
+constexpr double kExpBias = 0x1.8p20 + 0.5;
+struct Pow2 {
+  double p, s;
+};
+__device__ __forceinline__ Pow2 exp2_16th(double biased, const double* tab) {   // of y + kExpBias
+  const int hi = __double2hiint(biased);
+  const double f = __hiloint2double(0x43300000, __double2loint(biased)) - (0x1p52 + 0x1p31);
+  double p = fma(f, 0x1.3b29bf8ba0f3ap-23 * 0x1p-128, 0x1.c6b3f5b3946b2p-17 * 0x1p-96);
+  p = fma(p, f, 0x1.ebfbdfff31574p-11 * 0x1p-64);
+  p = fma(p, f, 0x1.62e42fec3f16fp-5 * 0x1p-32);
   p = fma(p, f, 1.0);
-  p *= tab[k & 15];
-  return __hiloint2double(__double2hiint(p) + ((k >> 4) << 20), __double2loint(p));
+  const double t = tab[hi & 15];
+  return {p, __hiloint2double(__double2hiint(t) + (hi << 16), __double2loint(t))};
 }
 
 template <typename T>
@@ -179,7 +185,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   uint32_t* bins = reinterpret_cast<uint32_t*>(zs0 + per + 4) + tid;
   const int run = pw / 32;                          // logits per thread: 4 .. 32, a multiple of kU
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  if (tid < 16) s.tab[tid] = kExpTab[tid];
+  if (tid < 16)
+    s.tab[tid] = __hiloint2double(__double2hiint(kExpTab[tid]) - (tid << 16), __double2loint(kExpTab[tid]));
   pdl_wait();
   pdl_trigger();
   const float* z = a.logits + (size_t)row * a.ld;
@@ -296,37 +303,31 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   const double inv_t = 1.0 / (double)T, md = (double)m;
   const double rate = inv_t * (16 / 0.693147180559945309417);
   // Logits below `floor` weigh nothing: less than e^-44 of the largest, 2^-46
-  // of the mass for all of a row.
-  const float floor = m - 44.f * T;
-  // y = 16 log2(e) (v - m) / T, in one fma where its rounding error, 2^-53 of
-  // m's share, is below 2^-37: |m| / T up to 4096
-  const bool near0 = fabsf(m) <= 4096.f * T;
-  const double y0 = -md * rate;
+  // of the mass for all of a row.  (-inf never weighs, however large T.)
+  const float floor = fmaxf(m - 44.f * T, -FLT_MAX);
   // N at a time, free of branches, so that they overlap; for v >= floor
-  auto weights = [&](auto& x, const auto& v) {
+  auto powers = [&](auto& x, const auto& v) {
     constexpr int N = sizeof(v) / sizeof(v[0]);
-    if (near0) {
 #pragma unroll
-      for (int u = 0; u < N; ++u) x[u] = fma((double)v[u], rate, y0);
-    } else {
-#pragma unroll
-      for (int u = 0; u < N; ++u) x[u] = ((double)v[u] - md) * rate;
-    }
-#pragma unroll
-    for (int u = 0; u < N; ++u) x[u] = exp2_16th(x[u], s.tab);
+    for (int u = 0; u < N; ++u) x[u] = exp2_16th(fma((double)v[u] - md, rate, kExpBias), s.tab);
+  };
+  auto power = [&](float v) -> Pow2 {
+    const float one[1] = {v};
+    Pow2 x[1];
+    powers(x, one);
+    return x[0];
   };
   auto weight = [&](float v) -> double {
-    const float one[1] = {v};
-    double x[1];
-    weights(x, one);
-    return x[0];
+    const Pow2 x = power(v);
+    return x.p * x.s;
   };
   // weights as integers of 43 bits, nearest (adding 2^52 leaves them in the
   // low bits of the double)
-  auto as_fixed = [&](double x) -> u64 {
-    return (u64)__double_as_longlong(fma(x, 0x1p43, 0x1p52)) & 0xfffffffffffffull;
+  auto as_fixed = [&](Pow2 x) -> u64 {
+    const double s43 = __hiloint2double(__double2hiint(x.s) + (43 << 20), __double2loint(x.s));
+    return (u64)__double_as_longlong(fma(x.p, s43, 0x1p52)) & 0xfffffffffffffull;
   };
-  auto fixed = [&](float v) { return as_fixed(weight(v)); };
+  auto fixed = [&](float v) { return as_fixed(power(v)); };
 
   // kept: z > cz, or z == cz and index <= ci
   float cz = -INFINITY;
@@ -474,6 +475,15 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     return true;
   };
 
+  // What a cutoff leaves out is taken out of the slice; each thread its logits.
+  auto exclude = [&] {
+    for (int q = 0; q < run; ++q) {
+      const int i = i0 + 32 * q;
+      const float v = zs[i];
+      if (v < cz || (v == cz && base + i > ci)) zs[i] = -INFINITY;
+    }
+  };
+
   // ---- one cutoff: by count (top-k) or by mass (top-p); true if the row is
   // finished --------------------------------------------------------------------
   auto select = [&](const bool by_mass) -> bool {
@@ -534,14 +544,13 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
             const int i = i0 + 32 * (q + u);
             v[u] = zs[i];
             in[u] = v[u] >= low;
-            if (cut && v[u] <= cz && !(v[u] == cz && base + i <= ci)) in[u] = false;
             any |= in[u];
           }
           uint32_t word = 0xffffffffu;
           if (__any_sync(0xffffffffu, any)) {
             int bn[kU];
-            double x[kU];
-            if (by_mass) weights(x, v);
+            Pow2 x[kU];
+            if (by_mass) powers(x, v);
             bins_of(bn, v);
 #pragma unroll
             for (int u = 0; u < kU; ++u)
@@ -756,6 +765,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     }
   };
   if (k < a.V) {
+    if (cut) exclude();
     if (select(false)) return;
     cut = true;
     lo = fmaxf(lo, cz);
@@ -775,6 +785,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     if (listed(mask, reinterpret_cast<Cand*>(bins - tid))) return;
   }
   if (topp < 1.f) {
+    if (cut) exclude();
     select(true);
     cut = true;
   }
@@ -784,24 +795,35 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   const float from = fmaxf(cz, floor);
   auto kept = [&](float v, int i) { return v >= from && (v > cz || (v == cz && base + i <= ci)); };
   double sum = 0.0;
-  uint32_t mask = 0;                   // this thread's kept logits
-  if (cut) {
-#pragma unroll 4
-    for (int q = 0; q < run; ++q) mask |= (uint32_t)kept(zs[i0 + 32 * q], i0 + 32 * q) << q;
-  }
-  if (cut && 3 * (int)__reduce_max_sync(0xffffffffu, (unsigned)__popc(mask)) < run) {
-    // few: each by itself (P = 0.9 of 64 x 131072: 54 -> 51 us)
-    for (uint32_t r = mask; r; r &= r - 1) sum += weight(zs[i0 + 32 * (__ffs(r) - 1)]);
-  } else {
+  if (!cut) {
     for (int q = 0; q < run; q += kU) {
       float v[kU];
-      double x[kU];
+      Pow2 x[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) v[u] = zs[i0 + 32 * (q + u)];
-      weights(x, v);                   // (of anything that is not kept)
+      powers(x, v);
 #pragma unroll
       for (int u = 0; u < kU; ++u)
-        if (cut ? mask >> (q + u) & 1 : v[u] >= from) sum += x[u];
+        if (v[u] >= floor) sum = fma(x[u].p, x[u].s, sum);
+    }
+  } else {
+    uint32_t mask = 0;                 // this thread's kept logits
+#pragma unroll 4
+    for (int q = 0; q < run; ++q) mask |= (uint32_t)kept(zs[i0 + 32 * q], i0 + 32 * q) << q;
+    if (3 * (int)__reduce_max_sync(0xffffffffu, (unsigned)__popc(mask)) < run) {
+      // few: each by itself (P = 0.9 of 64 x 131072: 54 -> 51 us)
+      for (uint32_t r = mask; r; r &= r - 1) sum += weight(zs[i0 + 32 * (__ffs(r) - 1)]);
+    } else {
+      for (int q = 0; q < run; q += kU) {
+        float v[kU];
+        Pow2 x[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) v[u] = zs[i0 + 32 * (q + u)];
+        powers(x, v);                  // (of anything that is not kept)
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (mask >> (q + u) & 1) sum = fma(x[u].p, x[u].s, sum);
+      }
     }
   }
   sum = wsum(sum);

@@ -24,7 +24,7 @@ def kept(z, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     order = np.lexsort((np.arange(V), -z))
     greedy = not temperature > 0
     with np.errstate(over="ignore", invalid="ignore"):
-        x = np.where(z == m, 0.0, np.where(z == -np.inf, -np.inf,
+        x = np.where(z == m, 0.0, np.where((z == -np.inf) | (m == np.inf), -np.inf,
                                            (z - m) / (1.0 if greedy else temperature)))
     ws = np.exp(x)[order]
     n = V

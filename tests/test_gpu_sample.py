@@ -109,6 +109,32 @@ def test_masked_rows_and_special_values():
     run(z, u, k=[4000] * B, mp=[0.001] * B)
 
 
+@pytest.mark.parametrize("T", [1e36, 1e37, 3e38, np.inf])
+def test_huge_temperatures_leave_masked_tokens_out(T):
+    """m - 44 T leaves f32's range; only finite logits (and +inf) may be drawn."""
+    rng = np.random.default_rng(11)
+    V, B = 5000, 6
+    z = logits(rng, B, V)
+    z[:, ::3] = -np.inf
+    z[1, 1::3] = np.nan
+    z[2, 300:] = -np.inf
+    z[3, 44] = np.inf
+    z[4, 100:200] = -3.0e38
+    z[5, 7], z[5, 8] = 3.0e38, -3.0e38
+    u = [0.0, 0.3, 0.999, 0.5, 0.7, 1.0]
+    # tokens below e^-44 of the largest weight are not drawn, not even by u = 1
+    # (row 5: e^-300 at T = 1e36), which the oracle would do
+    z64 = np.where(np.isnan(z), -np.inf, z.astype(np.float64))
+    m = z64.max(1, keepdims=True)
+    with np.errstate(invalid="ignore"):
+        drawn = np.where(((z64 - m) / float(np.float32(T)) < -44) | (z64 < m) & (m == np.inf),
+                         -np.inf, z)
+    on_gpu = torch.tensor(z, device="cuda")
+    for kw in ({}, dict(k=[900] * B), dict(p=[0.6] * B), dict(mp=[0.5] * B, p=[0.9] * B),
+               dict(k=[2000] * B, mp=[1e-3] * B, p=[0.8] * B)):
+        run(drawn, u, T=[T] * B, logits=on_gpu, **kw)
+
+
 def test_uniform_at_its_ends():
     rng = np.random.default_rng(8)
     z = logits(rng, 6, 3001)
