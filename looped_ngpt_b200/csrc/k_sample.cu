@@ -20,9 +20,10 @@
 // mass) is found by histograms of kNB linear bins over the range of the
 // logits still in question, narrowed until the bin that holds it has at most
 // kRank logits (or equal ones), which are then ranked exactly: two exchanges
-// per level, one or two levels unless the logits are adversarial.  A top-k
-// that leaves up to kRank logits is finished from one list of them.  Rows
-// without cutoffs need two exchanges.
+// per level, one or two levels unless the logits are adversarial.  The warps'
+// shares of what a top-p keeps come from the same histograms.  A top-k that
+// leaves up to kRank logits is finished from one list of them.  Rows without
+// cutoffs need one exchange and no copy in shared memory.
 //
 // Reading 64 x 131072 logits takes 5.1 us at the copy rate.  The kernel takes
 // 28 us without cutoffs, 51 us with top-p 0.9 and 37 us with top-k 50 and
@@ -94,6 +95,14 @@ __device__ __forceinline__ Pow2 exp2_16th(double biased, const double* tab) {   
   return {p, __hiloint2double(__double2hiint(t) + (hi << 16), __double2loint(t))};
 }
 
+// Values that are wanted here: not moved behind the branches that use them, where
+// they would wait for one another.
+template <int N>
+__device__ __forceinline__ void here(Pow2 (&x)[N]) {
+#pragma unroll
+  for (int u = 0; u < N; ++u) asm volatile("" : "+d"(x[u].p), "+d"(x[u].s));
+}
+
 template <typename T>
 __device__ __forceinline__ T wsum(T v) {
 #pragma unroll
@@ -114,6 +123,29 @@ struct Cand {
   int i;
   u64 w;
 };
+
+__device__ __forceinline__ double target_of(float u, double total) {
+  return (u > 0.f ? fmin((double)u, 1.0) : 0.0) * total;
+}
+
+// Which part of a sequence of shares holds the target: lane i has share x (0:
+// none); *start: what lies before it.  Past the end (u = 1): the last with any
+// mass.
+__device__ __forceinline__ int holder(double x, double from, double target, double* start) {
+  const int lane = threadIdx.x & 31;
+  double inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  const unsigned any = __ballot_sync(0xffffffffu, x > 0.0);
+  const unsigned hit = __ballot_sync(0xffffffffu, x > 0.0 && from + inc > target);
+  const int at = hit ? __ffs(hit) - 1 : 31 - __clz(any);
+  const double before = __shfl_up_sync(0xffffffffu, inc, 1);
+  *start = from + __shfl_sync(0xffffffffu, lane == 0 ? 0.0 : before, at);
+  return at;
+}
 
 // Shared memory of a block.  `Fixed`, then, with C blocks per row and slices
 // of `per` logits:
@@ -169,6 +201,178 @@ __host__ __device__ inline size_t sample_smem(int C, int per) {
 }
 static_assert(kRank * (2 * sizeof(Cand) + 8) <= kHistWords * 4, "lists fit the histograms' place");
 
+// The logit at which the running mass of a part of n <= N kSampThreads logits,
+// of which one at least is kept, passes the target (`start`: the mass before the
+// part): N neighbours per thread of the block; get(j), kept(v, j), weight(v);
+// one thread calls found(j, v).  m is any logit with a weight.
+template <int N, typename Get, typename Kept, typename Weight, typename Found>
+__device__ __forceinline__ void draw_in_part(Fixed& s, int n, double start, double target, Get get,
+                                             Kept kept, Weight weight, float m, Found found) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  double x[N], sum = 0.0;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int j = min(N * tid + u, n - 1);
+    const float v = get(j);
+    const bool in = N * tid + u < n && kept(v, j);
+    const double y = weight(in ? v : m);
+    x[u] = in ? y : 0.0;
+    sum += x[u];
+  }
+  const double mine = wsum(sum);
+  __syncthreads();                                  // dred has been read
+  if (lane == 0) s.dred[w] = mine;
+  __syncthreads();
+  if (holder(lane < kSW ? s.dred[lane] : 0.0, start, target, &start) != w) return;
+  if (holder(sum, start, target, &start) != lane) return;
+  int pick = -1;
+#pragma unroll
+  for (int u = 0; u < N; ++u)
+    if (x[u] > 0.0 && (pick < 0 || !(start > target))) {
+      pick = N * tid + u;
+      start += x[u];
+    }
+  found(pick, get(pick));
+}
+
+// ---- rows without cutoffs ---------------------------------------------------
+// One pass over the row in registers: each thread sums weights relative to the
+// largest of its logits so far; threads, warps and blocks are brought to the
+// row's largest when they are joined.  The part of one warp, which holds the
+// draw, is read again.
+__device__ __forceinline__ void draw_whole(const SampleArgs& a, Fixed& s, int row, int rank, int C,
+                                           int pw, float T, float uf) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int per = kSW * pw, base = rank * per;
+  const float* src = a.logits + (size_t)row * a.ld + base;
+  const int cnt = max(0, min(per, a.V - base));
+  // 16-byte chunks of the row: chunk j of the slice holds its logits 4 j - shift
+  // .. + 3; pw / 4 chunks per warp, and the last warp has what is left
+  const int shift = (int)((uintptr_t)src >> 2) & 3, j0 = w * (pw / 4);
+  const double inv_t = 1.0 / (double)T, rate = inv_t * (16 / 0.693147180559945309417);
+  auto floor_of = [&](float m) { return fmaxf(m - 44.f * T, -FLT_MAX); };
+  auto part = [&](double x, float m, float top) -> double {    // x of weights to m, to top
+    if (!(m >= floor_of(top))) return 0.0;
+    const Pow2 p = exp2_16th(fma((double)m - (double)top, rate, kExpBias), s.tab);
+    return x * (p.p * p.s);
+  };
+  auto load = [&](int j, float* v) {
+    const int i = 4 * j - shift;
+    if (i >= 0 && i + 4 <= cnt) {
+      const float4 f = *reinterpret_cast<const float4*>(src + i);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = i + u >= 0 && i + u < cnt ? src[i + u] : -INFINITY;
+    }
+  };
+  float top = -INFINITY;
+  double sum = 0.0;
+  constexpr int kQ = 4;                             // chunks at once
+  const int rounds = pw / 128 + (w == kSW - 1 && shift);
+  for (int t = 0; t < rounds; t += kQ) {
+    float v[4 * kQ];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      if (t + q < pw / 128)
+        load(j0 + lane + 32 * (t + q), v + 4 * q);
+      else if (t + q == pw / 128 && w == kSW - 1 && lane == 0)
+        load(j0 + 32 * (t + q), v + 4 * q);
+      else
+        v[4 * q] = v[4 * q + 1] = v[4 * q + 2] = v[4 * q + 3] = -INFINITY;
+    }
+    float big = v[0];
+#pragma unroll
+    for (int u = 1; u < 4 * kQ; ++u) big = fmaxf(big, v[u]);     // (passes over NaN)
+    if (big > top) {
+      sum = part(sum, top, big);
+      top = big;
+    }
+    const float from = floor_of(top);
+    const double td = (double)top;
+#pragma unroll
+    for (int g = 0; g < 4 * kQ; g += kU) {
+      Pow2 x[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        x[u] = exp2_16th(fma((double)v[g + u] - td, rate, kExpBias), s.tab);
+      here(x);
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (v[g + u] >= from) sum = fma(x[u].p, x[u].s, sum);
+    }
+  }
+  const uint32_t key = __reduce_max_sync(0xffffffffu, top > -INFINITY ? key_of(top + 0.f) : 0u);
+  auto top_of = [](uint32_t k) { return k ? key_float(k) : -INFINITY; };
+  sum = wsum(part(sum, top, top_of(key)));
+  if (lane == 0) {
+    s.ured[0][w] = key;
+    s.dred[w] = sum;
+  }
+  __syncthreads();
+  // every block has started: its shared memory may be written
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (w == 0) {
+    const uint32_t k = s.ured[0][lane & (kSW - 1)], all = __reduce_max_sync(0xffffffffu, k);
+    const double x = lane < kSW ? part(s.dred[lane], top_of(k), top_of(all)) : 0.0, t = wsum(x);
+    if (lane < C) {
+      put32(&s.ex.max[rank], lane, all);
+      put64(&s.ex.sum[rank], lane, __double_as_longlong(t));
+    }
+  }
+  cluster_sync_all();
+  const uint32_t bk = lane < C ? s.ex.max[lane] : 0u, mk = __reduce_max_sync(0xffffffffu, bk);
+  if (mk == 0) {                     // nothing to draw
+    if (rank == 0 && tid == 0) {
+      a.tokens[row] = -1;
+      if (a.logprobs) a.logprobs[row] = -INFINITY;
+    }
+    return;
+  }
+  const float m = key_float(mk), floor = floor_of(m);
+  const uint32_t wk = s.ured[0][lane & (kSW - 1)];
+  double share, of_warp;
+  const int lo = 4 * j0 - shift;                    // the first logit of the warp's part
+  if (m == INFINITY) {
+    // beside +inf nothing weighs anything
+    int n = 0;
+    for (int i = lo + lane; i < lo + pw + (w == kSW - 1 ? 4 : 0); i += 32)
+      n += i >= 0 && i < cnt && src[i] == m;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) s.dred[w] = n;
+    __syncthreads();
+    of_warp = lane < kSW ? s.dred[lane] : 0.0;
+    share = wsum(of_warp);
+    if (w == 0 && lane < C) put64(&s.ex.sum[rank], lane, __double_as_longlong(share));
+    cluster_sync_all();
+    share = lane < C ? s.ex.sum[lane] : 0.0;
+  } else {
+    share = lane < C ? part(s.ex.sum[lane], top_of(bk), m) : 0.0;
+    of_warp = lane < kSW ? part(s.dred[lane], top_of(wk), m) : 0.0;
+  }
+  const double total = wsum(share), target = target_of(uf, total), md = (double)m;
+  double start;
+  if (holder(share, 0.0, target, &start) != rank) return;
+  const int at = holder(of_warp, start, target, &start), first = at * pw - shift;
+  draw_in_part<3>(
+      s, pw + (at == kSW - 1 ? 4 : 0), start, target,
+      [&](int j) {
+        const int i = first + j;
+        return i >= 0 && i < cnt ? src[i] : -INFINITY;
+      },
+      [&](float v, int) { return m == INFINITY ? v == m : v >= floor; },
+      [&](float v) -> double {
+        const Pow2 p = exp2_16th(fma(v == m ? 0.0 : (double)v - md, rate, kExpBias), s.tab);
+        return p.p * p.s;
+      },
+      m,
+      [&](int j, float v) {
+        a.tokens[row] = base + first + j;
+        if (a.logprobs)
+          a.logprobs[row] = (float)((v == m ? 0.0 : ((double)v - md) * inv_t) - log(total));
+      });
+}
+
 __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, int C, int pw) {
   extern __shared__ __align__(16) uint8_t smraw[];
   Fixed& s = *reinterpret_cast<Fixed*>(smraw);
@@ -198,6 +402,11 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   minp = minp > 0.f ? fminf(minp, 1.f) : 0.f;
   const float uf = a.uniform[row];
   const bool cuts = k < a.V || topp < 1.f;
+  if (!greedy && !cuts && !(minp > 0.f)) {
+    __syncthreads();                                // the table
+    draw_whole(a, s, row, rank, C, pw, T, uf);
+    return;
+  }
 
   // ---- the slice, its largest and smallest finite logit ---------------------
   // In four parts, so that the first are looked at while the others arrive: a
@@ -475,6 +684,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     return true;
   };
 
+  u64 kept_mass = 0;                   // this thread's share of what top-p keeps
+
   // What a cutoff leaves out is taken out of the slice; each thread its logits.
   auto exclude = [&] {
     for (int q = 0; q < run; ++q) {
@@ -493,6 +704,15 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     low = fminf(low, hi);
     u64 mass_above = 0, want = 0;      // weights, or logits, before and up to the cutoff
     uint32_t mask = 0;                 // this thread's logits still in question
+    auto masked_kept = [&] {           // the mass of those of them that are kept
+      u64 f = 0;
+      for (uint32_t r = mask; r; r &= r - 1) {
+        const int i = i0 + 32 * (__ffs(r) - 1);
+        const float v = zs[i];
+        if (v > cz || (v == cz && base + i <= ci)) f += fixed(v);
+      }
+      return f;
+    };
     for (int level = 0;; ++level) {
       // histogram of the kept logits in [low, hi]
       // bin of (hi - v) sc, rounded (monotone; the ends fall into the first and
@@ -550,7 +770,10 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
           if (__any_sync(0xffffffffu, any)) {
             int bn[kU];
             Pow2 x[kU];
-            if (by_mass) powers(x, v);
+            if (by_mass) {
+              powers(x, v);
+              here(x);
+            }
             bins_of(bn, v);
 #pragma unroll
             for (int u = 0; u < kU; ++u)
@@ -623,6 +846,13 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       }
       mass_above = s.mass_above;
       want = s.want;
+      if (by_mass) {
+        // the warp's share of what lies above the bin
+#pragma unroll
+        for (int q = 0; q < kNB / 32; ++q)
+          if (kNB / 32 * lane + q < bin)
+            kept_mass += hist[kNB / 32 * lane + q] + ((u64)hist[kNB + kNB / 32 * lane + q] << 22);
+      }
       if (!by_mass && level == 0 && mass_above + s.bin_mass[bin] <= (u64)kRank) {
         // all logits down to the bin's end are few
         uint32_t upto = 0;
@@ -733,6 +963,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
         __syncthreads();
         cz = s.cut_z;
         ci = s.cut_i;
+        if (by_mass) kept_mass += masked_kept();
         return false;
       }
       if (low == hi) {
@@ -760,6 +991,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
         cluster_sync_all();
         cz = low;
         ci = s.ex.tie;
+        if (by_mass) kept_mass += masked_kept();
         return false;
       }
     }
@@ -795,23 +1027,14 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   const float from = fmaxf(cz, floor);
   auto kept = [&](float v, int i) { return v >= from && (v > cz || (v == cz && base + i <= ci)); };
   double sum = 0.0;
-  if (!cut) {
-    for (int q = 0; q < run; q += kU) {
-      float v[kU];
-      Pow2 x[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) v[u] = zs[i0 + 32 * (q + u)];
-      powers(x, v);
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if (v[u] >= floor) sum = fma(x[u].p, x[u].s, sum);
-    }
+  if (topp < 1.f) {
+    sum = (double)kept_mass * 0x1p-43;
   } else {
     uint32_t mask = 0;                 // this thread's kept logits
 #pragma unroll 4
     for (int q = 0; q < run; ++q) mask |= (uint32_t)kept(zs[i0 + 32 * q], i0 + 32 * q) << q;
     if (3 * (int)__reduce_max_sync(0xffffffffu, (unsigned)__popc(mask)) < run) {
-      // few: each by itself (P = 0.9 of 64 x 131072: 54 -> 51 us)
+      // few: each by itself
       for (uint32_t r = mask; r; r &= r - 1) sum += weight(zs[i0 + 32 * (__ffs(r) - 1)]);
     } else {
       for (int q = 0; q < run; q += kU) {
@@ -820,6 +1043,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
 #pragma unroll
         for (int u = 0; u < kU; ++u) v[u] = zs[i0 + 32 * (q + u)];
         powers(x, v);                  // (of anything that is not kept)
+        here(x);
 #pragma unroll
         for (int u = 0; u < kU; ++u)
           if (mask >> (q + u) & 1) sum = fma(x[u].p, x[u].s, sum);
@@ -834,56 +1058,20 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     if (lane < C) put64(&s.ex.sum[rank], lane, __double_as_longlong(t));
   }
   cluster_sync_all();
-  // Which part of a sequence of shares holds the target: lane i has share x
-  // (0: none); *start: what lies before it.  Past the end (u = 1): the last
-  // with any mass.
-  auto holder = [&](double x, double from, double target, double* start) {
-    double inc = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    const unsigned any = __ballot_sync(0xffffffffu, x > 0.0);
-    const unsigned hit = __ballot_sync(0xffffffffu, x > 0.0 && from + inc > target);
-    const int at = hit ? __ffs(hit) - 1 : 31 - __clz(any);
-    const double before = __shfl_up_sync(0xffffffffu, inc, 1);
-    *start = from + __shfl_sync(0xffffffffu, lane == 0 ? 0.0 : before, at);
-    return at;
-  };
   const double share = lane < C ? s.ex.sum[lane] : 0.0, total = wsum(share);
-  const double target = (uf > 0.f ? fmin((double)uf, 1.0) : 0.0) * total;
+  const double target = target_of(uf, total);
   double start;
   if (holder(share, 0.0, target, &start) != rank) return;
-  // the warp whose part holds it; its logits, two neighbours per thread of the
-  // block
+  // the warp whose part holds it
   const int part_of = holder(lane < kSW ? s.dred[lane] : 0.0, start, target, &start);
-  double x[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int j = 2 * tid + u, i = part_of * pw + min(j, pw - 1);
-    const float v = zs[i];
-    const bool in = j < pw && kept(v, i);
-    const double y = weight(in ? v : m);
-    x[u] = in ? y : 0.0;
-  }
-  const double two = wsum(x[0] + x[1]);
-  __syncthreads();                                  // dred has been read
-  if (lane == 0) s.dred[w] = two;
-  __syncthreads();
-  if (holder(lane < kSW ? s.dred[lane] : 0.0, start, target, &start) != w) return;
-  const int who = holder(x[0] + x[1], start, target, &start);
-  const double x0 = __shfl_sync(0xffffffffu, x[0], who), x1 = __shfl_sync(0xffffffffu, x[1], who);
-  const int token = part_of * pw + 2 * (32 * w + who) +
-                    (x0 == 0.0 || (x1 > 0.0 && !(start + x0 > target)));
-  if (lane == 0) {
-    a.tokens[row] = base + token;
-    if (a.logprobs) {
-      const float v = zs[token];
-      const double y = v == m ? 0.0 : ((double)v - md) * inv_t;
-      a.logprobs[row] = (float)(y - log(total));
-    }
-  }
+  draw_in_part<2>(
+      s, pw, start, target, [&](int j) { return zs[part_of * pw + j]; },
+      [&](float v, int j) { return kept(v, part_of * pw + j); }, weight, m,
+      [&](int j, float v) {
+        a.tokens[row] = base + part_of * pw + j;
+        if (a.logprobs)
+          a.logprobs[row] = (float)((v == m ? 0.0 : ((double)v - md) * inv_t) - log(total));
+      });
 }
 
 // ---- rows of any length ------------------------------------------------------
