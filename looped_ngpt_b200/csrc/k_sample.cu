@@ -8,9 +8,9 @@
 // the token is the first kept one in index order whose running mass exceeds
 // u times the kept mass.  Weights and sums are f64: a draw is decided by
 // which side of one of up to V borders u falls, and in f32 those borders are
-// off by more than neighbouring u differ.  (top-p's cutoff compares sums of
-// weights rounded to 2^-43 in 64-bit integers, whose order of addition is
-// free.)
+// off by more than neighbouring u differ.  (top-p's cutoff, and
+// the mass that it keeps, are sums of weights rounded to 2^-43 in 64-bit
+// integers, whose order of addition is free.)
 //
 // One thread-block cluster per row, up to 16 blocks: each keeps a slice of
 // the row in shared memory, read from HBM once, and the blocks exchange
@@ -26,15 +26,23 @@
 // cutoffs need one exchange and no copy in shared memory.
 //
 // Reading 64 x 131072 logits takes 5.1 us at the copy rate.  The kernel takes
-// 28 us without cutoffs, 51 us with top-p 0.9 and 37 us with top-k 50 and
-// top-p 0.95 (13.5 us for one such row): two waves of eight-block clusters
-// (64 KB of logits and 45 KB of exchange per block, two blocks per SM), each
-// a chain of exchanges of 0.7 us and, per logit, 60 instructions in all
-// without cutoffs and 115 with a top-p; issue slots are 55% busy, the f64 pipe
-// 11 to 20%.  Measured and not kept: 16-block clusters of 8192 logits for many
-// rows (40 / 95 us where 8-block ones took 28.5 / 58), 256 threads with 128
-// registers (30 / 60 against the same), one copy of the cutoff code for both
-// kinds (29 / 55 against 28 / 51).
+// 23 us without cutoffs, 47 us with top-p 0.9 and 35 us with top-k 50 and
+// top-p 0.95 (13 us for one such row, 5.9 us for one without): two waves of
+// eight-block clusters (64 KB of logits and 45 KB of exchange per block, two
+// blocks per SM).  Without cutoffs half of a wave's 10 us are the weights (44
+// instructions per logit, of them 8 f64, which run at 60 lanes per clock and
+// SM), the rest the launch, the first loads, one exchange and the draw.  With a
+// top-p (97 instructions) a third is the first histogram, where shared memory
+// is the limit (two atomics per logit at 13 lanes per clock, less what
+// conflicts cost), and two thirds a chain of steps that each take 0.3 to 1.5
+// us, six of them exchanges of 0.7 us.
+//
+// Measured and not kept: 16-block clusters of 8192 logits for many rows (40 /
+// 95 us where 8-block ones took 28.5 / 58), 256 threads with 128 registers (30
+// / 60 against the same), one copy of the cutoff code for both kinds (29 / 55
+// against 28 / 51), the bin and the blocks' shares found by every warp, and
+// candidates sent by those that find them (three barriers and one exchange
+// less: 48 against 47).
 #include "async_copy.cuh"
 #include "common.cuh"
 
@@ -93,14 +101,6 @@ __device__ __forceinline__ Pow2 exp2_16th(double biased, const double* tab) {   
   p = fma(p, f, 1.0);
   const double t = tab[hi & 15];
   return {p, __hiloint2double(__double2hiint(t) + (hi << 16), __double2loint(t))};
-}
-
-// Values that are wanted here: not moved behind the branches that use them, where
-// they would wait for one another.
-template <int N>
-__device__ __forceinline__ void here(Pow2 (&x)[N]) {
-#pragma unroll
-  for (int u = 0; u < N; ++u) asm volatile("" : "+d"(x[u].p), "+d"(x[u].s));
 }
 
 template <typename T>
@@ -291,15 +291,9 @@ __device__ __forceinline__ void draw_whole(const SampleArgs& a, Fixed& s, int ro
     const float from = floor_of(top);
     const double td = (double)top;
 #pragma unroll
-    for (int g = 0; g < 4 * kQ; g += kU) {
-      Pow2 x[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-        x[u] = exp2_16th(fma((double)v[g + u] - td, rate, kExpBias), s.tab);
-      here(x);
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if (v[g + u] >= from) sum = fma(x[u].p, x[u].s, sum);
+    for (int u = 0; u < 4 * kQ; ++u) {
+      const Pow2 x = exp2_16th(fma((double)v[u] - td, rate, kExpBias), s.tab);
+      if (v[u] >= from) sum = fma(x.p, x.s, sum);
     }
   }
   const uint32_t key = __reduce_max_sync(0xffffffffu, top > -INFINITY ? key_of(top + 0.f) : 0u);
@@ -431,6 +425,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
+  const double inv_t = 1.0 / (double)T, rate = inv_t * (16 / 0.693147180559945309417);
   float vmax = -INFINITY, vmin = INFINITY;          // of what may be drawn
   auto look = [&](float v) {
     vmax = fmaxf(vmax, v);                          // (passes over NaN)
@@ -509,8 +504,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     m = lo = 0.f;
     kmax = key_of(m);
   }
-  const double inv_t = 1.0 / (double)T, md = (double)m;
-  const double rate = inv_t * (16 / 0.693147180559945309417);
+  const double md = (double)m;
   // Logits below `floor` weigh nothing: less than e^-44 of the largest, 2^-46
   // of the mass for all of a row.  (-inf never weighs, however large T.)
   const float floor = fmaxf(m - 44.f * T, -FLT_MAX);
@@ -770,10 +764,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
           if (__any_sync(0xffffffffu, any)) {
             int bn[kU];
             Pow2 x[kU];
-            if (by_mass) {
-              powers(x, v);
-              here(x);
-            }
+            if (by_mass) powers(x, v);
             bins_of(bn, v);
 #pragma unroll
             for (int u = 0; u < kU; ++u)
@@ -1043,7 +1034,6 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
 #pragma unroll
         for (int u = 0; u < kU; ++u) v[u] = zs[i0 + 32 * (q + u)];
         powers(x, v);                  // (of anything that is not kept)
-        here(x);
 #pragma unroll
         for (int u = 0; u < kU; ++u)
           if (mask >> (q + u) & 1) sum = fma(x[u].p, x[u].s, sum);
