@@ -189,6 +189,16 @@ class DoryModel:
         None to draw it from torch's generator.  Returns the new tokens int32
         [B, n_new], and their log-probabilities f32 [B, n_new] if `logprobs`.
         Runs on the current stream and waits for it once, at the end."""
+        home = self.device
+        if (not isinstance(prompt, torch.Tensor) or prompt.dim() != 2
+                or prompt.dtype is not torch.int32 or not prompt.is_contiguous()
+                or prompt.device.type != home.type
+                or home.index not in (None, prompt.device.index)
+                or 0 in prompt.shape):
+            raise ValueError(f"prompt: contiguous int32 [B, T] on {home} is needed")
+        if n_new < 0 or (uniform is not None
+                         and uniform.shape != (n_new, prompt.shape[0])):
+            raise ValueError("n_new >= 0 and uniform [n_new, B] are needed")
         B, T = prompt.shape
         dev = prompt.device
 

@@ -218,14 +218,15 @@ class KV8Pages:
             n = _dense(n, "n", _I32, (B,), dev).data_ptr()
         if T == 0:
             return
-        # the stride arrays of the last call, if the strides are the same
+        # the stride arrays of the last call (of any thread), if the strides are
+        # the same
         key = (T, k.stride(), v.stride())
         pk, pv = k.data_ptr(), v.data_ptr()
-        if key != self._rows[0] or pk % 16 or pv % 16:
-            self._rows = (key, _I64x3(*_rows(k, "k", 3)),
-                          _I64x3(*_rows(v, "v", 3)))
-        _, ks, vs = self._rows
-        args = (self._ref, pk, pv, ks, vs, T, pos.data_ptr(), n)
+        rows = self._rows
+        if key != rows[0] or pk % 16 or pv % 16:
+            rows = self._rows = (key, _I64x3(*_rows(k, "k", 3)),
+                                 _I64x3(*_rows(v, "v", 3)))
+        args = (self._ref, pk, pv, rows[1], rows[2], T, pos.data_ptr(), n)
         st = _here(dev) if stream is None else None
         if st is not None:
             rc = _lib.load().dory_kv8_append(*args, st)
@@ -267,19 +268,20 @@ class KV8Pages:
         if window < 0:
             raise ValueError("window: 0 (off) or more is needed")
         key, pq = q.stride(), q.data_ptr()
-        if key != self._q_rows[0] or pq % 16:
-            self._q_rows = (key, _I64x2(*_rows(q, "q", 2)))
+        rows = self._q_rows
+        if key != rows[0] or pq % 16:
+            rows = self._q_rows = (key, _I64x2(*_rows(q, "q", 2)))
         if out is not None:
             _dense(out, "out", _BF16, shape, dev)
         if scale is None:
             scale = hd ** -0.5
         st = _here(dev) if stream is None else None
         if st is not None:
-            return self._attend(st, pq, q, lens, window, scale, out, ws)
+            return self._attend(st, pq, rows[1], q, lens, window, scale, out, ws)
         with _On(dev, stream) as st:
-            return self._attend(st, pq, q, lens, window, scale, out, ws)
+            return self._attend(st, pq, rows[1], q, lens, window, scale, out, ws)
 
-    def _attend(self, st, pq, q, lens, window, scale, out, ws):
+    def _attend(self, st, pq, strides, q, lens, window, scale, out, ws):
         Hq = q.shape[1]
         if out is None:
             out = (torch.empty_like(q) if q.is_contiguous()
@@ -291,7 +293,7 @@ class KV8Pages:
             if ws is None:
                 ws = self._ws[st, Hq] = self.workspace(Hq)
         rc = _lib.load().dory_kv8_attend(
-            self._ref, pq, self._q_rows[1], Hq, lens.data_ptr(), window, scale,
+            self._ref, pq, strides, Hq, lens.data_ptr(), window, scale,
             out.data_ptr(), ws.data_ptr(), ws.numel(), st)
         if rc:
             check("dory_kv8_attend", rc)

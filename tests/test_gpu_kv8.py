@@ -300,6 +300,40 @@ def test_attend_strided_query_given_buffers_and_streams():
     assert all(torch.equal(o, ref) for pair in outs for o in pair)
 
 
+def test_threads_with_unlike_strides():
+    """Two threads on one cache, each with its own stream and query layout."""
+    import sys
+    import threading
+
+    rng = np.random.default_rng(25)
+    lens = [70, 128, 1]
+    pages, codes, scales, table = filled(rng, lens, 2, 2, 64)
+    fused = bf(rng.standard_normal((3, 3, 8, 64))).cuda()
+    qs = [fused[:, 1], fused[:, 2].contiguous()]
+    ls = i32(lens)
+    want = [pages.attend(q, ls).clone() for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        outs = [pages.attend(qs[i], ls, stream=streams[i]) for _ in range(200)]
+        streams[i].synchronize()
+        bad.extend(i for o in outs if not torch.equal(o, want[i]))
+
+    before = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(before)
+    assert not bad
+
+
 def test_shared_prefix_pages():
     """Two sequences read the same first page and own their last ones."""
     rng = np.random.default_rng(23)

@@ -318,3 +318,14 @@ def test_generate(tiny, kv_fmt):
                 assert torch.equal(tok, am) and torch.all(l == 0)
             z, am = gm.decode_step(cache, tok, k, ws)
     assert gm.generate(prompt, 3, k, temperature=1.0).shape == (B, 3)
+
+
+def test_generate_refusals(tiny):
+    _, gm = tiny
+    p = torch.from_numpy(make_prompt(TINY, 2, 12, seed=66)).cuda()
+    u = torch.rand(3, 2, device="cuda")
+    for prompt, kw in ((p.long(), {}), (p.cpu(), {}), (p[0], {}), (p[:, ::2], {}),
+                       (p[:, :0], {}), (p, dict(uniform=u[:2])), (p, dict(uniform=u.t()))):
+        with pytest.raises(ValueError):
+            gm.generate(prompt, 3, 2, **kw)
+    assert gm.generate(p, 0, 2).shape == (2, 0)
