@@ -158,6 +158,19 @@ def test_strided_rows_given_outputs_and_empty_batch():
     assert t.shape == (0,) and lp is None
 
 
+@pytest.mark.parametrize("V", [262143, 262144, 262145])
+def test_around_the_largest_cluster(V):
+    """The longest rows a cluster holds, flat and peaked, and one logit more."""
+    rng = np.random.default_rng(V)
+    B = 4
+    z = np.stack([logits(rng, 1, V, p)[0] for p in (0.0, 0.7, 1.5, 3.0)])
+    z[0] = 0.5                              # all equal
+    u = rng.random(B)
+    for kw in ({}, dict(p=[0.9] * B), dict(k=[50] * B, p=[0.95] * B), dict(k=[200000] * B),
+               dict(mp=[0.01] * B, p=[0.5] * B)):
+        run(z, u, T=[0.8] * B, **kw)
+
+
 def test_large_vocabulary():
     """Rows too large for the shared memory of one cluster."""
     rng = np.random.default_rng(10)
