@@ -17,6 +17,12 @@
 // a fence and a counter per pair, took 3 to 8 us longer than the dependent
 // launch, at every size.)
 //
+// Where there are few pairs of short sequences each pair gets a cluster of up
+// to 16 thread blocks instead, which share its blocks in the same way and join
+// their pieces in each other's shared memory: one launch, no prefix sum over
+// the lengths (head_dim 160, 4 KV heads, against runs: 1 sequence of 2048 7.1
+// for 9.2 us, 16 of 1024 9.5 for 12.0 us).
+//
 // One block in a warp: S^T = K Q^T on m16n8k16 (keys as A rows, the heads as
 // the 8 columns), online softmax per head (lane 4g + t owns heads 2t, 2t+1),
 // P^T by an in-register transpose, O^T += V^T P^T.  Codes become f16 in
@@ -39,9 +45,9 @@
 //
 // Times (head_dim 160, 4 query heads per KV head, 4 KV heads, of 6.55 TB/s):
 // 64 sequences of 32768 tokens 414 us (99%), 4 of 131072 114 us (90%), one of
-// 2048 8.2 us, a chain of lengths -> page -> tile -> product -> join.  48 sequences of up
-// to 9001 tokens behind a 1024-token window (head_dim 128, 8 x 8 heads) take
-// 32 us (46%): 10 blocks per warp do not amortise that chain.
+// 2048 7 us, a chain of length -> page -> tile -> product -> join.  48 sequences
+// of up to 9001 tokens behind a 1024-token window (head_dim 128, 8 x 8 heads)
+// take 32 us (46%): 10 blocks per warp do not amortise that chain.
 #include <algorithm>
 
 #include "async_copy.cuh"
@@ -59,6 +65,7 @@ constexpr long kPolls = 1L << 18;
 constexpr float kShift = 9.f;                 // weights are p * 2^9 ...
 constexpr float kSlack = 4.f;                 // ... and at most 2^4 more
 constexpr int kNear = 2, kFar = 60;           // V scale / unit: in p; in f32
+constexpr int kMaxC = 16;                     // thread blocks per pair
 
 // 2^x on the SFU (subnormal results flush to zero).
 __device__ __forceinline__ float ex2(float x) {
@@ -81,6 +88,9 @@ struct Att {
   static constexpr int NST = HD == 160 ? 1 : 2;
   static constexpr size_t smem(int B) {
     return 1024 + (size_t)NW * NST * STAGE + (size_t)(2 * B + 1) * 4;
+  }
+  static constexpr size_t smem_pair(int G) {
+    return 1024 + (size_t)NW * NST * STAGE + (size_t)(G * HD + 2 * kMaxC * G) * 4;
   }
 };
 
@@ -125,9 +135,11 @@ __device__ __forceinline__ int visible_blocks(const Kv8AttendArgs& a, int b) {
   return (len + kKv8Block - 1) / kKv8Block - lo / kKv8Block;
 }
 
-template <int HD, int G>
+// PAIR: one pair per cluster of thread blocks, which share its blocks and join
+// their pieces through each other's shared memory: no second kernel.
+template <int HD, int G, bool PAIR>
 __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
-    const __grid_constant__ Kv8Maps maps, const Kv8AttendArgs a) {
+    const __grid_constant__ Kv8Maps maps, const Kv8AttendArgs a, int C) {
   using L = Att<HD>;
   constexpr int KS = L::KS, NST = L::NST, NW = L::NW, kThreads = 32 * NW;
   constexpr int PART = kPart<HD, G>;
@@ -141,6 +153,8 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
 
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int B = a.B, H = a.c.Hkv;
+  const int rank = PAIR ? (int)blockIdx.x % C : 0, own = PAIR ? (int)blockIdx.x / C : 0;   // pair
+  if (PAIR) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   uint64_t* full = full_[w];
   int4* meta = meta_[w];
   if (lane == 0) {
@@ -151,42 +165,56 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
   pdl_trigger();
   fence_proxy_async_global();          // rows that earlier kernels wrote
 
-  // prefix of blocks per sequence
-  for (int b0 = 0, run = 0; b0 < B; b0 += kThreads) {
-    const int b = b0 + tid;
-    int n = 0;
-    if (b < B) {
-      lens[b] = length_of(a, b);
-      if (blockIdx.x == 0 && lens[b] != a.len[b]) atomicOr(a.err, ERRBIT_BOUNDS);
-      n = visible_blocks(a, b);
+  int X0, X1;                          // this thread block's run
+  int own_len = 0, own_nb = 0;         // PAIR: the pair's length and blocks
+  if (PAIR) {
+    const int b = own / H;
+    own_len = length_of(a, b);
+    own_nb = visible_blocks(a, b);
+    if (tid == 0 && rank == 0 && own == b * H && own_len != a.len[b])
+      atomicOr(a.err, ERRBIT_BOUNDS);
+    const int per = (own_nb + C - 1) / C;
+    X0 = min(own_nb, rank * per);
+    X1 = min(own_nb, X0 + per);
+  } else {
+    // prefix of blocks per sequence
+    for (int b0 = 0, run = 0; b0 < B; b0 += kThreads) {
+      const int b = b0 + tid;
+      int n = 0;
+      if (b < B) {
+        lens[b] = length_of(a, b);
+        if (blockIdx.x == 0 && lens[b] != a.len[b]) atomicOr(a.err, ERRBIT_BOUNDS);
+        n = visible_blocks(a, b);
+      }
+      int inc = n;
+  #pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      __syncthreads();
+      if (lane == 31) wsum[w] = inc;
+      __syncthreads();
+      int base = run;
+      for (int i = 0; i < NW; ++i) {
+        if (i < w) base += wsum[i];
+        run += wsum[i];
+      }
+      if (b < B) pre[b + 1] = base + inc;
     }
-    int inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
+    if (tid == 0) pre[0] = 0;
     __syncthreads();
-    if (lane == 31) wsum[w] = inc;
-    __syncthreads();
-    int base = run;
-    for (int i = 0; i < NW; ++i) {
-      if (i < w) base += wsum[i];
-      run += wsum[i];
-    }
-    if (b < B) pre[b + 1] = base + inc;
+    const int total = pre[B] * H;
+    const int per = (total + gridDim.x - 1) / gridDim.x;
+    X0 = (int)min((int64_t)total, (int64_t)blockIdx.x * per);
+    X1 = min(total, X0 + per);
   }
-  if (tid == 0) pre[0] = 0;
-  __syncthreads();
-  const int total = pre[B] * H;
-  const int per = (total + gridDim.x - 1) / gridDim.x;
-  const int X0 = (int)min((int64_t)total, (int64_t)blockIdx.x * per), X1 = min(total, X0 + per);
   const int perw = (X1 - X0 + NW - 1) / NW;
   const int x0 = min(X1, X0 + w * perw), x1 = min(X1, x0 + perw);
   float* ws_block = reinterpret_cast<float*>(a.ws);
   float* ws_warp = ws_block + (size_t)2 * gridDim.x * PART + (size_t)blockIdx.x * NW * PART;
   if (lane < 2) s_piece[2 * w + lane] = -1;
-  for (int b = blockIdx.x; b < B; b += gridDim.x)      // empty sequences
+  for (int b = blockIdx.x; !PAIR && b < B; b += gridDim.x)      // empty sequences
     if (pre[b + 1] == pre[b])
       for (int i = tid; i < H * G * HD; i += kThreads)
         a.out[(size_t)b * H * G * HD + i] = __float2bfloat16_rn(0.f);
@@ -202,12 +230,17 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
   };
   // first linear block of a pair, and its number of blocks
   auto start_of = [&](int pair, int* nb) {
+    if (PAIR) {
+      *nb = own_nb;
+      return 0;
+    }
     const int b = pair / H, h = pair - b * H;
     *nb = pre[b + 1] - pre[b];
     return pre[b] * H + h * *nb;
   };
+  auto held = [&](int b) { return PAIR ? own_len : lens[b]; };
   auto first_block = [&](int b) {
-    return a.window ? max(0, lens[b] - a.window) / kKv8Block : 0;
+    return a.window ? max(0, held(b) - a.window) / kKv8Block : 0;
   };
 
   // ---- this warp's items: blocks x0 + m ------------------------------------
@@ -222,8 +255,18 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
       plan_u = -1;
       plan.x = -1;                     // no block: a bad page
       if (x < x1) {
-        const int b = seq_of(x), nb = pre[b + 1] - pre[b], r = x - pre[b] * H;
-        const int h = r / nb, j = r - h * nb + first_block(b);
+        int b, h, j;
+        if (PAIR) {
+          b = own / H;
+          h = own - b * H;
+          j = x;
+        } else {
+          b = seq_of(x);
+          const int nb = pre[b + 1] - pre[b], r = x - pre[b] * H;
+          h = r / nb;
+          j = r - h * nb;
+        }
+        j += first_block(b);
         const int page = a.c.block_table[(size_t)b * a.c.pages_per_seq + (j >> 1)];
         plan.y = b * H + h;
         if (page < 0 || page >= a.c.n_pages) {
@@ -272,7 +315,7 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
         // workspace
         int nb;
         const int xs = start_of(pair, &nb);
-        const bool whole = xs >= x0 && xs + nb <= x1, last = it.y < 0;
+        const bool whole = !PAIR && xs >= x0 && xs + nb <= x1, last = it.y < 0;
         float* part = last ? reinterpret_cast<float*>(st_ptr) : ws_warp + w * PART;
         if (!whole && lane == 0) s_piece[2 * w + (x0 < xs)] = 2 * pair + last;
         // eu = 0: no block was read
@@ -304,7 +347,7 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
       if (it.y < 0) break;
       pair = it.y;
       const int b = pair / H, h = pair - b * H;
-      len = lens[b];
+      len = held(b);
       lo = a.window ? max(0, len - a.window) : 0;
       eu = 0;
       m2[0] = m2[1] = -INFINITY;
@@ -505,6 +548,81 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
   if (id >= 0)
     mine = id & 1 ? reinterpret_cast<const float*>(stages + (size_t)(lane >> 1) * NST * L::STAGE)
                   : ws_warp + (lane >> 1) * PART;
+  // one head of a pair from the pieces of lanes `of`: its max, sum and output
+  float M, Ls;
+  float4 O[NV];
+  auto join = [&](bool in, unsigned of, int head) {
+    const float m = in ? mine[G * HD + head] : -INFINITY;
+    const float l = in ? mine[G * HD + G + head] : 0.f;
+    M = warp_max(m);
+    const float f = m == -INFINITY ? 0.f : ex2(m - M);
+    Ls = warp_sum(l * f);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) O[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (unsigned r = of; r; r &= r - 1) {
+      const int k = __ffs(r) - 1;
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      const float* q = reinterpret_cast<const float*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), k)) + head * HD;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int d = 4 * (lane + 32 * v);
+        if (d < HD) {
+          const float4 y = *reinterpret_cast<const float4*>(q + d);
+          O[v].x = fmaf(fk, y.x, O[v].x);
+          O[v].y = fmaf(fk, y.y, O[v].y);
+          O[v].z = fmaf(fk, y.z, O[v].z);
+          O[v].w = fmaf(fk, y.w, O[v].w);
+        }
+      }
+    }
+  };
+  if (PAIR) {
+    // The cluster's pieces: block r gets outputs r n .. (r + 1) n - 1 of all of
+    // them, and every block all maxima and sums.
+    const int n = G * HD / C;
+    float* got = reinterpret_cast<float*>(stages + NW * NST * L::STAGE);   // [C][n]
+    float* got_m = got + G * HD;                                           // [C][2][G]
+    auto put = [&](const float* p, int r, float v) {
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(p, r)), "f"(v) : "memory");
+    };
+    const unsigned of = __ballot_sync(0xffffffffu, id >= 0);
+    // every block has started: its shared memory may be written
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int head = w; head < G; head += NW) {
+      join(id >= 0, of, head);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int d = 4 * (lane + 32 * v);
+        if (d >= HD) continue;
+        const float x[4] = {O[v].x, O[v].y, O[v].z, O[v].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = head * HD + d + i, r = e / n;
+          put(got + rank * n + e - r * n, r, x[i]);
+        }
+      }
+      if (lane < C) {
+        put(got_m + (2 * rank) * G + head, lane, M);
+        put(got_m + (2 * rank + 1) * G + head, lane, Ls);
+      }
+    }
+    cluster_sync_all();
+    for (int i = tid; i < n; i += kThreads) {
+      const int e = rank * n + i, head = e / HD;
+      float top = -INFINITY, l = 0.f, x = 0.f;
+      for (int c = 0; c < C; ++c) top = fmaxf(top, got_m[2 * c * G + head]);
+      for (int c = 0; c < C; ++c) {
+        const float m = got_m[2 * c * G + head], f = m == -INFINITY ? 0.f : ex2(m - top);
+        l = fmaf(f, got_m[(2 * c + 1) * G + head], l);
+        x = fmaf(f, got[c * n + i], x);
+      }
+      const size_t to = (size_t)own * G * HD + e;
+      const float y = l == 0.f ? 0.f : x / l;
+      a.out[to] = __float2bfloat16_rn(a.gate ? a.gate[to] * y : y);
+    }
+    return;
+  }
   unsigned left = __ballot_sync(0xffffffffu, id >= 0);
   for (int task = 0; left;) {
     const int pr = __shfl_sync(0xffffffffu, id >> 1, __ffs(left) - 1);
@@ -517,29 +635,7 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
     float* part = ws_block + (size_t)(2 * blockIdx.x + (X0 < xs)) * PART;
     for (int head = 0; head < G; ++head, ++task) {
       if (task % NW != w) continue;
-      const float m = in ? mine[G * HD + head] : -INFINITY;
-      const float l = in ? mine[G * HD + G + head] : 0.f;
-      const float M = warp_max(m), f = m == -INFINITY ? 0.f : ex2(m - M), Ls = warp_sum(l * f);
-      float4 O[NV];
-#pragma unroll
-      for (int v = 0; v < NV; ++v) O[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (unsigned r = of; r; r &= r - 1) {
-        const int k = __ffs(r) - 1;
-        const float fk = __shfl_sync(0xffffffffu, f, k);
-        const float* q = reinterpret_cast<const float*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), k)) + head * HD;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int d = 4 * (lane + 32 * v);
-          if (d < HD) {
-            const float4 y = *reinterpret_cast<const float4*>(q + d);
-            O[v].x = fmaf(fk, y.x, O[v].x);
-            O[v].y = fmaf(fk, y.y, O[v].y);
-            O[v].z = fmaf(fk, y.z, O[v].z);
-            O[v].w = fmaf(fk, y.w, O[v].w);
-          }
-        }
-      }
+      join(in, of, head);
       const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -690,25 +786,81 @@ int attend_grid() {
   return n[dev];
 }
 
+// What a device takes of one instantiation: set up once (twice, if two threads
+// meet here).
+struct Fit {
+  bool set;
+  int clusters[5];                     // at a time, of 1, 2, 4, 8 and 16 thread blocks
+};
+
+template <int HD, int G>
+Fit fit_of() {
+  using L = Att<HD>;
+  static Fit fit[kMaxDevices];
+  int dev = 0;
+  const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices;
+  if (known && fit[dev].set) return fit[dev];
+  Fit f = {};
+  cudaFuncSetAttribute(kv8_attend_kernel<HD, G, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)L::smem(kKv8MaxBatch));
+  auto k = kv8_attend_kernel<HD, G, true>;
+  const size_t smem = L::smem_pair(G);
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) ==
+      cudaSuccess) {
+    const bool wide =
+        cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    for (int i = 0; i < (wide ? 5 : 4); ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(1 << i, 1, 1);
+      cfg.blockDim = dim3(32 * L::NW);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 1 << i;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess) f.clusters[i] = n;
+    }
+  }
+  cudaGetLastError();
+  f.set = true;
+  if (known) fit[dev] = f;
+  return f;
+}
+
 template <int HD, int G>
 void attend_t(const Kv8AttendArgs& a, const Kv8Maps& maps, cudaStream_t st) {
   using L = Att<HD>;
+  const Fit fit = fit_of<HD, G>();
+  const int64_t pairs = (int64_t)a.B * a.c.Hkv;
   const int grid = attend_grid();
-  const size_t smem = L::smem(a.B);
-  // once per device: shared memory for the largest batch
-  static bool set[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || !set[dev]) {
-    cudaFuncSetAttribute(kv8_attend_kernel<HD, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)L::smem(kKv8MaxBatch));
-    if (dev >= 0 && dev < kMaxDevices) set[dev] = true;
+  // Few pairs of short sequences: one cluster each, the largest that lets all
+  // of them run at once.  It saves 2 to 3 us, but a thread block streams its
+  // share of the longest sequence, whatever the others' lengths, and SMs are
+  // left over: taken while that share is at most 128 KB more than an SM's share
+  // of all pairs, at half the longest length.  (Equal lengths, head_dim 160, 64
+  // SMs in clusters: 9.2 for 10.0 us at 96 KB more, 12.3 for 11.7 at 256 KB;
+  // head_dim 64: 8.8 for 10.4 us at 100 KB, 12.0 for 12.5 at 200 KB.)
+  int i = 4;
+  while (i >= 0 && pairs > fit.clusters[i]) --i;
+  int64_t blocks = 2ll * a.c.pages_per_seq;            // at most visible
+  if (a.window) blocks = std::min<int64_t>(blocks, (a.window - 1) / kKv8Block + 2);
+  if (i >= 0 &&
+      ((double)blocks / (1 << i) - 0.5 * pairs * blocks / grid) * L::STAGE <= 128 * 1024) {
+    launch_k_cluster(kv8_attend_kernel<HD, G, true>, dim3((unsigned)pairs << i),
+                     dim3(32 * L::NW), L::smem_pair(G), st, 1 << i, maps, a, 1 << i);
+    return;
   }
-  launch_k(kv8_attend_kernel<HD, G>, dim3(grid), dim3(32 * L::NW), smem, st, maps, a);
+  launch_k(kv8_attend_kernel<HD, G, false>, dim3(grid), dim3(32 * L::NW), L::smem(a.B), st, maps,
+           a, 1);
   // the fewer pairs, the more pieces each may have
-  const int pairs = a.B * a.c.Hkv;
   const bool few = pairs <= 64;
   const int heads = few ? 1 : G, warps = few ? (pairs <= 16 ? 16 : 8) : std::max(8, G);
-  launch_k(kv8_merge_kernel<HD, G>, dim3(pairs, G / heads), dim3(32, warps), 0, st, a, grid, heads);
+  launch_k(kv8_merge_kernel<HD, G>, dim3((unsigned)pairs, G / heads), dim3(32, warps), 0, st, a,
+           grid, heads);
 }
 
 template <int HD>

@@ -55,6 +55,21 @@ def pages_of(codes, scales, table):
     return lb.KV8Pages(t(codes[0]), t(codes[1]), t(scales[0]), t(scales[1]), t(table))
 
 
+@pytest.fixture(params=["pairs", "runs"])
+def layout(request, monkeypatch):
+    """attend takes a cluster per pair where the block table is short, and
+    equal runs over all pairs where it is long: the same pages behind both."""
+    if request.param == "runs":
+        short = pages_of
+
+        def long(codes, scales, table):
+            more = np.zeros((len(table), 5000), np.int32)
+            return short(codes, scales, np.concatenate([table, more], axis=1))
+
+        monkeypatch.setitem(globals(), "pages_of", long)
+    return request.param
+
+
 def i32(a):
     return torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)
 
@@ -198,7 +213,7 @@ def check_attend(out, q, codes, scales, table, lens, window, scale):
 
 @pytest.mark.parametrize("hd,H,G", [(64, 2, 1), (64, 1, 8), (128, 1, 2), (128, 2, 8),
                                     (160, 1, 4), (160, 2, 8), (160, 1, 1)])
-def test_attend_lengths_and_windows(hd, H, G):
+def test_attend_lengths_and_windows(hd, H, G, layout):
     rng = np.random.default_rng(hd + G)
     lens = [0, 1, 31, 32, 33, 63, 64, 65, 127, 200, 700]
     pages, codes, scales, table = filled(rng, lens, 11, H, hd)
@@ -212,7 +227,7 @@ def test_attend_lengths_and_windows(hd, H, G):
     check_attend(pages.attend(q, i32(short), scale=-0.3), q, codes, scales, table, short, 0, -0.3)
 
 
-def test_attend_long_and_many():
+def test_attend_long_and_many(layout):
     rng = np.random.default_rng(20)
     lens = [9000, 3, 4097]
     pages, codes, scales, table = filled(rng, lens, 141, 1, 160)
@@ -226,7 +241,7 @@ def test_attend_long_and_many():
     check_attend(pages.attend(q, i32(lens)), q, codes, scales, table, lens, 0, 64 ** -0.5)
 
 
-def test_attend_unlike_scales_and_query_magnitudes():
+def test_attend_unlike_scales_and_query_magnitudes(layout):
     """V blocks whose scales differ by 2^60, the larger ones with weight ~0 or
     not; queries from 2^-40 to 2^30 (their scores stay moderate)."""
     rng = np.random.default_rng(21)
@@ -258,7 +273,7 @@ def test_attend_unlike_scales_and_query_magnitudes():
     check_attend(pages.attend(q, i32([256]), scale=1.0), q, codes, scales, table[:1], [256], 0, 1.0)
 
 
-def test_attend_small_weights_add_up():
+def test_attend_small_weights_add_up(layout):
     """One key of weight 1 and 8000 of weight e^-16 each: together they are
     a thousandth of the answer, and none may be lost to rounding."""
     hd, n = 64, 8001
@@ -279,7 +294,7 @@ def test_attend_small_weights_add_up():
     assert np.all(np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -10) * want)
 
 
-def test_attend_strided_query_given_buffers_and_streams():
+def test_attend_strided_query_given_buffers_and_streams(layout):
     rng = np.random.default_rng(22)
     lens = [100, 64, 5]
     pages, codes, scales, table = filled(rng, lens, 2, 2, 128)
@@ -300,7 +315,7 @@ def test_attend_strided_query_given_buffers_and_streams():
     assert all(torch.equal(o, ref) for pair in outs for o in pair)
 
 
-def test_threads_with_unlike_strides():
+def test_threads_with_unlike_strides(layout):
     """Two threads on one cache, each with its own stream and query layout."""
     import sys
     import threading
@@ -334,7 +349,7 @@ def test_threads_with_unlike_strides():
     assert not bad
 
 
-def test_shared_prefix_pages():
+def test_shared_prefix_pages(layout):
     """Two sequences read the same first page and own their last ones."""
     rng = np.random.default_rng(23)
     codes, scales, table = pool(rng, 2, 3, 1, 64)
@@ -407,6 +422,39 @@ def test_bad_pages_positions_and_lengths_are_reported(model):
     out = pages_of(codes, scales, bad).attend(q, i32([128, 128, 128]))
     assert model.sync_status() == -7
     check_attend(out, q, codes, scales, table, [64, 64, 128], 0, 0.125)
+
+
+def test_bad_pages_and_lengths_in_long_tables(model, layout):
+    rng = np.random.default_rng(26)
+    B = 5
+    pages, codes, scales, table = filled(rng, [128] * B, 2, 2, 160)
+    q = bf(rng.standard_normal((B, 8, 160))).cuda()
+    lens = [128, 128, 10 ** 6, -5, 90]
+    bad = table.copy()
+    bad[0, 1], bad[1, 0], bad[4, 0], bad[4, 1] = len(codes[0]), -1, -7, 2 ** 31 - 1
+    out = pages_of(codes, scales, bad).attend(q, i32(lens))
+    assert model.sync_status() == -7
+    assert torch.all(out[2:] == 0)
+    check_attend(out[:1], q[:1], codes, scales, table[:1], [64], 0, 160 ** -0.5)
+    # (the second page alone, as a sequence of its own)
+    check_attend(out[1:2], q[1:2], codes, scales, table[1:2, 1:], [64], 0, 160 ** -0.5)
+
+
+@pytest.mark.parametrize("hd,H,G", [(160, 4, 4), (128, 8, 8), (64, 1, 1), (64, 4, 2)])
+def test_attend_pairs_over_the_range(hd, H, G):
+    """From one pair to more than a device runs at once, at lengths on both
+    sides of every split between thread blocks and warps."""
+    rng = np.random.default_rng(hd * G)
+    for B in (1, 2, 5, 17, 40):
+        lens = [int(x) for x in rng.integers(0, 1200, B)]
+        lens[0] = 1200
+        pages, codes, scales, table = filled(rng, lens, 19, H, hd)
+        q = bf(rng.standard_normal((B, H * G, hd))).cuda()
+        for window in (0, 100):
+            out = pages.attend(q, i32(lens), window=window)
+            check_attend(out, q, codes, scales, table, lens, window, hd ** -0.5)
+            again = pages.attend(q, i32(lens), window=window)
+            assert torch.equal(out, again)
 
 
 def test_refusals():
