@@ -26,8 +26,8 @@
 // cutoffs need one exchange and no copy in shared memory.
 //
 // Reading 64 x 131072 logits takes 5.1 us at the copy rate.  The kernel takes
-// 23 us without cutoffs, 47 us with top-p 0.9 and 35 us with top-k 50 and
-// top-p 0.95 (13 us for one such row, 5.9 us for one without): two waves of
+// 23 us without cutoffs, 45 us with top-p 0.9 and 34 us with top-k 50 and
+// top-p 0.95 (12 us for one such row, 5.9 us for one without): two waves of
 // eight-block clusters (64 KB of logits and 45 KB of exchange per block, two
 // blocks per SM).  Without cutoffs half of a wave's 10 us are the weights (44
 // instructions per logit, of them 8 f64, which run at 60 lanes per clock and
@@ -35,7 +35,10 @@
 // top-p (97 instructions) a third is the first histogram, where shared memory
 // is the limit (two atomics per logit at 13 lanes per clock, less what
 // conflicts cost), and two thirds a chain of steps that each take 0.3 to 1.5
-// us, six of them exchanges of 0.7 us.
+// us, six of them exchanges of 0.7 us.  Much of the code runs once, as fast as
+// it can be fetched, so short loops are kept as loops where that is shorter
+// (unrolled by the compiler's choice: 13.2 for 12.2 us with one row of top-k
+// 50, 47 for 45 with 64 of top-p 0.9).
 //
 // Measured and not kept: 16-block clusters of 8192 logits for many rows (40 /
 // 95 us where 8-block ones took 28.5 / 58), 256 threads with 128 registers (30
@@ -271,6 +274,7 @@ __device__ __forceinline__ void draw_whole(const SampleArgs& a, Fixed& s, int ro
   double sum = 0.0;
   constexpr int kQ = 4;                             // chunks at once
   const int rounds = pw / 128 + (w == kSW - 1 && shift);
+#pragma unroll 1
   for (int t = 0; t < rounds; t += kQ) {
     float v[4 * kQ];
 #pragma unroll
@@ -417,6 +421,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
   const int rounds = (chunks + kSampThreads - 1) / kSampThreads, part = (rounds + 3) / 4;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
+#pragma unroll 1
     for (int t = g * part; t < (g + 1) * part; ++t) {
       const int i = tid + t * kSampThreads;
       if (i < chunks)
@@ -440,6 +445,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     if (g == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
     if (g == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
     if (g == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll 1
     for (int t = g * part; t < (g + 1) * part; ++t) {
       const int i = tid + t * kSampThreads;
       if (i < chunks) {
@@ -716,7 +722,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       const float span = hi - low;
       const bool f32 = span > 1e-30f && span < 1e30f;
       const float sf = f32 ? (float)kNB / span : 0.f;
-      const double hd = (double)hi, sc = low == hi ? 0.0 : (double)kNB / (hd - (double)low);
+      const double hd = (double)hi, sc = f32 || low == hi ? 0.0 : (double)kNB / (hd - (double)low);
       auto bins_of = [&](auto& q, const auto& v) {      // for v <= hi
         constexpr int N = sizeof(v) / sizeof(v[0]);
         if (f32) {
@@ -751,6 +757,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
         if (by_mass) atomicAdd(hist + kNB + bn, (uint32_t)(f >> 22));
       };
       if (level == 0) {
+#pragma unroll 1
         for (int q = 0; q < run; q += kU) {
           float v[kU];
           bool in[kU], any = false;
@@ -791,6 +798,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
           f1 += hist_all[j * 2 * kNB + kNB + tid];
         }
         const u64 f = f0 + (f1 << 22);
+#pragma unroll 1
         for (int c = 0; c < C; ++c) put64(ex_mass + rank * kNB + tid, c, f);
       }
       cluster_sync_all();
@@ -848,6 +856,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       if (!by_mass && level == 0 && mass_above + s.bin_mass[bin] <= (u64)kRank) {
         // all logits down to the bin's end are few
         uint32_t upto = 0;
+#pragma unroll 1
         for (int q = 0; q < run; q += kU) {
           const uint32_t e = __vcmpleu4(bins[(q / kU) * kSampThreads], bin * 0x01010101u) & 0x08040201u;
           upto |= ((e | e >> 8 | e >> 16 | e >> 24) & 15u) << q;
@@ -859,6 +868,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
       }
       // the bin's logits
       if (level == 0) {
+#pragma unroll 1
         for (int q = 0; q < run; q += kU) {
           const uint32_t e = __vcmpeq4(bins[(q / kU) * kSampThreads], bin * 0x01010101u) & 0x08040201u;
           mask |= ((e | e >> 8 | e >> 16 | e >> 24) & 15u) << q;
@@ -1023,12 +1033,13 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     sum = (double)kept_mass * 0x1p-43;
   } else {
     uint32_t mask = 0;                 // this thread's kept logits
-#pragma unroll 4
+#pragma unroll 1
     for (int q = 0; q < run; ++q) mask |= (uint32_t)kept(zs[i0 + 32 * q], i0 + 32 * q) << q;
     if (3 * (int)__reduce_max_sync(0xffffffffu, (unsigned)__popc(mask)) < run) {
       // few: each by itself
       for (uint32_t r = mask; r; r &= r - 1) sum += weight(zs[i0 + 32 * (__ffs(r) - 1)]);
     } else {
+#pragma unroll 1
       for (int q = 0; q < run; q += kU) {
         float v[kU];
         Pow2 x[kU];
