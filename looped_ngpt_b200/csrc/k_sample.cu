@@ -32,7 +32,7 @@
 // blocks per SM).  Without cutoffs half of a wave's 10 us are the weights (44
 // instructions per logit, of them 8 f64, which run at 60 lanes per clock and
 // SM), the rest the launch, the first loads, one exchange and the draw.  With a
-// top-p (97 instructions) a third is the first histogram, where shared memory
+// top-p (95 instructions) a third is the first histogram, where shared memory
 // is the limit (two atomics per logit at 13 lanes per clock, less what
 // conflicts cost), and two thirds a chain of steps that each take 0.3 to 1.5
 // us, six of them exchanges of 0.7 us.  Much of the code runs once, as fast as
