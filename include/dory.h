@@ -410,8 +410,9 @@ int dory_kv8_append(const dory_kv8* c, const void* d_k, const void* d_v,
  * sums are f32.  L = 0 gives zeros.  Rows at positions >= L may hold
  * anything.  n_q_heads / n_kv_heads must be 1, 2, 4 or 8.
  *   - d_ws: dory_kv8_workspace_bytes, 256-byte aligned; its contents between
- *     calls are meaningless.  Calls that may run at the same time need
- *     workspaces of their own.
+ *     calls are meaningless.  Calls that may run, or be enqueued by two
+ *     threads, at the same time need workspaces of their own (a call is up to
+ *     two launches, the second of which reads what the first left there).
  *   - A length outside 0..64 * pages_per_seq counts as 0, and a page index
  *     outside 0..n_pages-1 hides that page's keys; both are reported as
  *     DORY_ERR_DEVICE by dory_sync_status of any model.

@@ -8,6 +8,7 @@ device's current stream).  Arguments that do not fit raise ``ValueError``
 before anything is enqueued.
 """
 import ctypes
+import threading
 
 import torch
 
@@ -179,7 +180,10 @@ class KV8Pages:
         plan = -(-ctypes.addressof(self._plan) // 64) * 64
         check("dory_kv8_plan", _lib.load().dory_kv8_plan(self._ref, plan))
         self.c.plan = plan
-        self._ws = {}
+        # workspaces by (stream, heads).  A call is two launches, the second of
+        # which reads what the first left in the workspace, and the interpreter
+        # lock is let go meanwhile: held over both
+        self._ws, self._ws_lock = {}, threading.Lock()
         self._rows = self._q_rows = (None,)
         self._q_heads = [g * shape[1] for g in (1, 2, 4, 8)]
 
@@ -252,8 +256,9 @@ class KV8Pages:
         head_dim], over the lens[b] (int32 [batch]) cached tokens, the last
         `window` of them if window > 0; scale defaults to 1 / sqrt(head_dim).
         Returns bf16 [batch, n_q_heads, head_dim] (`out`, if given).  Without
-        `ws` this object keeps one workspace per stream, and a captured graph
-        gets one of its own."""
+        `ws` this object keeps one workspace per stream (threads may share the
+        stream), and a captured graph gets one of its own; a `ws` given is for
+        one thread and one stream at a time."""
         dev, B, hd = self.device, self.batch, self.head_dim
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q: bf16 [batch, n_q_heads, head_dim] is needed")
@@ -288,13 +293,19 @@ class KV8Pages:
                    else torch.empty(q.shape, dtype=_BF16, device=self.device))
         if ws is None and torch.cuda.is_current_stream_capturing():
             ws = self.workspace(Hq)          # the graph's own
-        elif ws is None:
+        if ws is not None:
+            self._enqueue(st, pq, strides, Hq, lens, window, scale, out, ws)
+            return out
+        with self._ws_lock:
             ws = self._ws.get((st, Hq))
             if ws is None:
                 ws = self._ws[st, Hq] = self.workspace(Hq)
+            self._enqueue(st, pq, strides, Hq, lens, window, scale, out, ws)
+        return out
+
+    def _enqueue(self, st, pq, strides, Hq, lens, window, scale, out, ws):
         rc = _lib.load().dory_kv8_attend(
             self._ref, pq, strides, Hq, lens.data_ptr(), window, scale,
             out.data_ptr(), ws.data_ptr(), ws.numel(), st)
         if rc:
             check("dory_kv8_attend", rc)
-        return out

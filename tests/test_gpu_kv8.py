@@ -536,3 +536,37 @@ def test_decode_steps_together_and_captured():
         z = zbuf.cpu().numpy()
         for b in range(B):
             assert int(tok[b]) == osample.sample_row(z[b], uu[b], top_p=float(np.float32(0.9)))[0]
+
+
+def test_threads_on_one_stream(layout):
+    """Two threads on one cache and one stream, with the kept workspace."""
+    import sys
+    import threading
+
+    rng = np.random.default_rng(27)
+    lens = [70, 128, 100]
+    pages, codes, scales, table = filled(rng, lens, 2, 2, 64)
+    qs = [bf(rng.standard_normal((3, 8, 64))).cuda() for _ in range(2)]
+    ls = i32(lens)
+    want = [pages.attend(q, ls).clone() for q in qs]
+    for q, o in zip(qs, want):
+        check_attend(o, q, codes, scales, table, lens, 0, 0.125)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        outs = [pages.attend(qs[i], ls) for _ in range(300)]
+        torch.cuda.current_stream().synchronize()
+        bad.extend(i for o in outs if not torch.equal(o, want[i]))
+
+    before = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(before)
+    assert not bad

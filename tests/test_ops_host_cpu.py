@@ -1,0 +1,72 @@
+"""Host side of KV8Pages with a stand-in for the library (no GPU): which
+strides, sizes and workspaces the entry points get, and in which order calls of
+several threads are enqueued."""
+import contextlib
+import threading
+import time
+
+import pytest
+import torch
+
+from looped_ngpt_b200 import ops
+
+BF16 = torch.bfloat16
+
+
+class StandIn:
+    """Notes what each call gets.  Attention is enqueued as two launches, with
+    time for another thread between them, as outside the interpreter lock."""
+
+    def __init__(self):
+        self.strides, self.launches, self.windows = [], [], []
+
+    def dory_kv8_plan(self, c, plan):
+        return 0
+
+    def dory_kv8_workspace_bytes(self, c, n_q_heads, out):
+        out._obj.value = 512
+        return 0
+
+    def dory_kv8_attend(self, c, q, strides, n_q_heads, lens, window, scale, out, ws, nb, st):
+        self.strides.append(list(strides))
+        self.windows.append(window)
+        self.launches.append((ws, "attend", out))
+        time.sleep(0.002)
+        self.launches.append((ws, "merge", out))
+        return 0
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    lib = StandIn()
+    monkeypatch.setattr(ops, "_cuda", lambda t, name: t.device)
+    monkeypatch.setattr(ops, "_here", lambda device: 0)
+    monkeypatch.setattr(ops._lib, "load", lambda: lib)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return lib
+
+
+def pages(heads=1, batch=3):
+    return ops.KV8Pages.empty(batch, 64, heads, 64, device="cpu")
+
+
+def test_threads_on_one_stream_do_not_mix_their_launches(lib):
+    """The kept workspace carries pieces from the attention to the kernel that
+    joins them: no other call on the stream may come between the two."""
+    p, lens = pages(), torch.zeros(3, dtype=torch.int32)
+
+    def work():
+        q = torch.zeros(3, 4, 64, dtype=BF16)
+        for _ in range(5):
+            p.attend(q, lens)
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(lib.launches) == 30
+    assert len({ws for ws, _, _ in lib.launches}) == 1
+    for a, m in zip(lib.launches[::2], lib.launches[1::2]):
+        assert (a[1], m[1]) == ("attend", "merge") and a[2] == m[2]
