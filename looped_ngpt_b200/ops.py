@@ -272,7 +272,7 @@ class KV8Pages:
         _dense(lens, "lens", _I32, (B,), dev)
         if window < 0:
             raise ValueError("window: 0 (off) or more is needed")
-        key, pq = q.stride(), q.data_ptr()
+        key, pq = (Hq, q.stride()), q.data_ptr()
         rows = self._q_rows
         if key != rows[0] or pq % 16:
             rows = self._q_rows = (key, _I64x2(*_rows(q, "q", 2)))

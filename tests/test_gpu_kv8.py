@@ -570,3 +570,14 @@ def test_threads_on_one_stream(layout):
     finally:
         sys.setswitchinterval(before)
     assert not bad
+
+
+def test_one_head_then_more_of_one_buffer(layout):
+    """Queries of the same strides with 1 and with 8 heads, in turn."""
+    rng = np.random.default_rng(28)
+    lens = [100, 64, 5]
+    pages, codes, scales, table = filled(rng, lens, 2, 1, 64)
+    buf = bf(rng.standard_normal((3, 8, 64))).cuda()
+    for G in (1, 8, 1, 2):
+        q = buf[:, :G]
+        check_attend(pages.attend(q, i32(lens)), q, codes, scales, table, lens, 0, 0.125)

@@ -70,3 +70,20 @@ def test_threads_on_one_stream_do_not_mix_their_launches(lib):
     assert len({ws for ws, _, _ in lib.launches}) == 1
     for a, m in zip(lib.launches[::2], lib.launches[1::2]):
         assert (a[1], m[1]) == ("attend", "merge") and a[2] == m[2]
+
+
+def test_strides_of_one_head_are_not_kept_for_more(lib):
+    """A dim of length 1 has no stride of its own, so calls with the same
+    strides and another number of heads do not share stride arrays."""
+    p, lens = pages(), torch.zeros(3, dtype=torch.int32)
+    buf = torch.zeros(3, 8, 64, dtype=BF16)
+    p.attend(buf[:, :1], lens)
+    p.attend(buf, lens)
+    p.attend(buf[:, :1], lens)
+    assert lib.strides == [[512, 0], [512, 64], [512, 0]]
+    # a head stride that one head does not use, and more do
+    odd = torch.zeros(3 * 8 * 68, dtype=BF16).as_strided((3, 8, 64), (544, 68, 1))
+    p.attend(odd[:, :1], lens)
+    with pytest.raises(ValueError, match="aligned"):
+        p.attend(odd, lens)
+    assert len(lib.strides) == 4
