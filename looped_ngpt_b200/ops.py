@@ -17,6 +17,7 @@ from ._lib import DoryKv8, check
 
 PAGE = 64                 # tokens per page
 BLOCK = 32                # tokens per scale
+LIMIT = 2 ** 31           # sizes are 32-bit in the library
 
 _I64x3 = ctypes.c_int64 * 3
 _I64x2 = ctypes.c_int64 * 2
@@ -104,6 +105,8 @@ def sample(logits, uniform, temperature=None, top_k=None, top_p=None,
         ld = V
     if V < 1 or (V > 1 and step != 1) or ld < V:
         raise ValueError("logits: rows must be contiguous and apart")
+    if B >= LIMIT or V >= LIMIT:
+        raise ValueError("logits: fewer than 2^31 rows and columns are needed")
     row = row[:1]
     _dense(uniform, "uniform", _F32, row, dev)
     T = k = p = m = None
@@ -167,6 +170,8 @@ class KV8Pages:
                tuple(block_table.shape), dev)
         if 0 in shape or 0 in block_table.shape:
             raise ValueError("an empty cache")
+        if max(*shape, *block_table.shape) >= LIMIT:
+            raise ValueError("fewer than 2^31 pages and sequences are needed")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.block_table, self.device = block_table, dev
         self.n_kv_heads, self.head_dim = shape[1], shape[3]
@@ -272,6 +277,7 @@ class KV8Pages:
         _dense(lens, "lens", _I32, (B,), dev)
         if window < 0:
             raise ValueError("window: 0 (off) or more is needed")
+        window = min(window, self.pages_per_seq * PAGE)
         key, pq = (Hq, q.stride()), q.data_ptr()
         rows = self._q_rows
         if key != rows[0] or pq % 16:

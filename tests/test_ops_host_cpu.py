@@ -87,3 +87,29 @@ def test_strides_of_one_head_are_not_kept_for_more(lib):
     with pytest.raises(ValueError, match="aligned"):
         p.attend(odd, lens)
     assert len(lib.strides) == 4
+
+
+def test_windows_past_32_bits(lib):
+    """A window of the whole cache or more is the whole cache, however large."""
+    p, lens = pages(), torch.zeros(3, dtype=torch.int32)
+    q = torch.zeros(3, 4, 64, dtype=BF16)
+    for w in (0, 5, 64, 65, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 70):
+        p.attend(q, lens, window=w)
+    assert lib.windows == [0, 5] + [64] * 6
+    with pytest.raises(ValueError, match="window"):
+        p.attend(q, lens, window=-2 ** 32)
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    """Sizes that the library's 32-bit arguments would cut (no memory behind
+    these tensors)."""
+    def meta(*shape, dtype=torch.float32):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    for B, V in ((1, 2 ** 31), (1, 2 ** 32 + 5), (2 ** 32 + 1, 3)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            ops.sample(meta(B, V), meta(B))
+    for n, H, B, P in ((2 ** 32 + 2, 1, 1, 2), (2, 1, 2 ** 32 + 1, 1), (2, 1, 1, 2 ** 31)):
+        codes, scales = meta(n, H, 64, 64, dtype=torch.uint8), meta(n, H, 2)
+        with pytest.raises(ValueError, match="2\\^31"):
+            ops.KV8Pages(codes, codes, scales, scales, meta(B, P, dtype=torch.int32))
