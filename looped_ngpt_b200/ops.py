@@ -284,6 +284,9 @@ class KV8Pages:
             rows = self._q_rows = (key, _I64x2(*_rows(q, "q", 2)))
         if out is not None:
             _dense(out, "out", _BF16, shape, dev)
+        if ws is not None and not (isinstance(ws, torch.Tensor) and ws.dtype is torch.uint8
+                                   and ws.device == dev and ws.is_contiguous()):
+            raise ValueError(f"ws: contiguous uint8 on {dev} is needed (workspace())")
         if scale is None:
             scale = hd ** -0.5
         st = _here(dev) if stream is None else None

@@ -113,3 +113,18 @@ def test_sizes_past_32_bits_are_refused(lib):
         codes, scales = meta(n, H, 64, 64, dtype=torch.uint8), meta(n, H, 2)
         with pytest.raises(ValueError, match="2\\^31"):
             ops.KV8Pages(codes, codes, scales, scales, meta(B, P, dtype=torch.int32))
+
+
+def test_workspaces_that_do_not_fit(lib):
+    """A workspace is bytes in one piece on the cache's device; anything else
+    would have the kernels write to memory that is not theirs."""
+    p, lens = pages(), torch.zeros(3, dtype=torch.int32)
+    q = torch.zeros(3, 4, 64, dtype=BF16)
+    ws = p.workspace(4)
+    for bad in (ws.view(torch.int32), ws.to("meta"), torch.zeros(2 * ws.numel(), dtype=torch.uint8)[::2],
+                ws.numpy(), ws.data_ptr()):
+        with pytest.raises(ValueError, match="ws"):
+            p.attend(q, lens, ws=bad)
+    assert not lib.launches
+    p.attend(q, lens, ws=ws)
+    assert lib.launches[0][0] == ws.data_ptr()
