@@ -31,10 +31,14 @@
 // largest lose bits that f32 sums would lose too).  Weights are f16, 11 bits:
 // p * 2^9 against a reference max that moves only when a score passes it by
 // 2^4 (any common reference gives the same o; so most blocks need no
-// rescaling and no reduction across lanes, just one vote), and none above
-// 2^-33 of the largest is lost.  K's scale joins the score's factor; V's
-// scale, relative to the unit O is held in, joins the exponent of p when
-// within 2^2, else the block's product is added in f32.
+// rescaling and no reduction across lanes, just one vote).  K's scale joins the
+// score's factor.  V's scale, relative to the unit O is held in, joins the
+// exponent of p when within 2^2: an f16 weight below 2^-23 of the largest is
+// then off by up to 2^-34 of it.  The unit is the smallest scale so far, so
+// that such an error meets small values.  Blocks of larger scales have their
+// weights scaled by their own largest first and their product added in f32:
+// what is light may count as much as the rest by its values, down to weights of
+// 2^-126 of the largest (f32).
 //
 // Row r = 8 i + perm(g) of a block (i < 4) is fragment row g.  Tiles carry the
 // swizzle of their row width (128, 64 or 32 bytes), and perm lets two
@@ -64,7 +68,11 @@ namespace {
 constexpr long kPolls = 1L << 18;
 constexpr float kShift = 9.f;                 // weights are p * 2^9 ...
 constexpr float kSlack = 4.f;                 // ... and at most 2^4 more
-constexpr int kNear = 2, kFar = 60;           // V scale / unit: in p; in f32
+constexpr int kNear = 2;                      // V scale within 2^this of O's unit: in p
+constexpr int kFar = 36;                      // V scales 2^+-this: sums fit f32 in any unit
+constexpr int kPlain = 256 + 127 + (int)kShift;
+// Exponent field of O's unit for V's scale.
+__device__ __forceinline__ int unit_for(int ev) { return abs(ev - 127) <= kFar ? ev : kPlain; }
 constexpr int kMaxC = 16;                     // thread blocks per pair
 
 // 2^x on the SFU (subnormal results flush to zero).
@@ -72,6 +80,11 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 2^e for e <= 127 (subnormal ones too, then 0).
+__device__ __forceinline__ float pow2i(int e) {
+  return __uint_as_float(e >= -126 ? (uint32_t)(e + 127) << 23 : e >= -149 ? 1u << (e + 149) : 0u);
 }
 
 template <int HD>
@@ -305,7 +318,7 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
   uint32_t qf[KS][2];
   float hs[2] = {0.f, 0.f};            // score factors of heads 2t, 2t + 1
   float m2[2], c2[2], l2[2], o[KS][4]; // reference max, kShift - it, sum, output
-  int eu = 0;                          // O is held in units of 2^(eu - 127)
+  int eu = 0;                          // O is held in units of 2^((eu & 255) - 127)
   for (;; ++n) {
     const int4 it = n < items ? meta[s] : make_int4(0, -1, 0, 0);
     if (it.y < 0 || it.y != pair) {
@@ -318,8 +331,7 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
         const bool whole = !PAIR && xs >= x0 && xs + nb <= x1, last = it.y < 0;
         float* part = last ? reinterpret_cast<float*>(st_ptr) : ws_warp + w * PART;
         if (!whole && lane == 0) s_piece[2 * w + (x0 < xs)] = 2 * pair + last;
-        // eu = 0: no block was read
-        const float unit = eu ? __uint_as_float((uint32_t)(eu - (int)kShift) << 23) : 0.f;
+        const float unit = pow2i((eu & 255) - 127 - (int)kShift);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
@@ -349,7 +361,7 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
       const int b = pair / H, h = pair - b * H;
       len = held(b);
       lo = a.window ? max(0, len - a.window) : 0;
-      eu = 0;
+      eu = unit_for((uint32_t)it.w >> 23);
       m2[0] = m2[1] = -INFINITY;
       c2[0] = c2[1] = INFINITY;
       l2[0] = l2[1] = 0.f;
@@ -428,18 +440,20 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
                        kv8_f16x2(kw[3][i] >> 16), qf[k][0], qf[k][1]);
         }
       }
-      // V's scale against O's unit
+      // V's scale against O's unit, which is the smallest scale so far (up to
+      // 2^kNear), or 2^kShift (plain units) once one lies outside 2^+-kFar
       const int ev = (uint32_t)it.w >> 23;
-      if (eu == 0) eu = abs(ev - 127) <= kFar ? ev : 127 + (int)kShift;
-      if (abs(ev - eu) > kFar) {       // from here on O in plain units
-        const float f = __uint_as_float((uint32_t)(eu - (int)kShift) << 23);
+      bool near = abs(ev - eu) <= kNear;
+      if (!near && eu != kPlain && (ev < eu || abs(ev - 127) > kFar)) {
+        const int to = unit_for(ev);
+        const float f = pow2i(eu - (to & 255));
 #pragma unroll
         for (int d = 0; d < KS; ++d)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[d][i] *= f;
-        eu = 127 + (int)kShift;
+        eu = to;
+        near = ev == to;
       }
-      const bool near = abs(ev - eu) <= kNear;
       const float lr = near ? (float)(ev - eu) : 0.f;
 
       const float ks = __int_as_float(it.z), f0 = hs[0] * ks, f1 = hs[1] * ks;
@@ -492,6 +506,22 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
       const float ir = near ? __uint_as_float((uint32_t)(127 + eu - ev) << 23) : 1.f;
       l2[0] = fmaf((p[0][0] + p[1][0]) + (p[2][0] + p[3][0]), ir, l2[0]);   // this lane's keys
       l2[1] = fmaf((p[0][1] + p[1][1]) + (p[2][1] + p[3][1]), ir, l2[1]);
+      // Far blocks: each head's weights are brought to [2^8, 2^9) by its largest
+      // one, so that the f16 ones keep their 11 bits however light the block is
+      int eh[2] = {0, 0};
+      if (!near) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float mx = fmaxf(fmaxf(p[0][hh], p[1][hh]), fmaxf(p[2][hh], p[3][hh]));
+#pragma unroll
+          for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+          const int e = (int)(__float_as_uint(mx) >> 23) - 127 - 8;      // p is 0, or normal
+          eh[hh] = mx > 0.f && mx < INFINITY ? max(e, -126) : 0;
+          const float f = __uint_as_float((uint32_t)(127 - eh[hh]) << 23);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i][hh] *= f;
+        }
+      }
       uint32_t pb[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -514,13 +544,13 @@ __global__ void __launch_bounds__(32 * Att<HD>::NW, 1) kv8_attend_kernel(
 #pragma unroll
         for (int d = 0; d < KS; ++d) add_pv(d, o[d]);
       } else {
-        const float f = __uint_as_float((uint32_t)ev << 23) * __uint_as_float((uint32_t)(254 - eu) << 23);
+        const float f0 = pow2i(ev - (eu & 255) + eh[0]), f1 = pow2i(ev - (eu & 255) + eh[1]);
 #pragma unroll
         for (int d = 0; d < KS; ++d) {
           float tt[4] = {0.f, 0.f, 0.f, 0.f};
           add_pv(d, tt);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[d][i] = fmaf(tt[i], f, o[d][i]);
+          for (int i = 0; i < 4; ++i) o[d][i] = fmaf(tt[i], i & 1 ? f1 : f0, o[d][i]);
         }
       }
       if (edge) fence_proxy_async_smem();

@@ -581,3 +581,52 @@ def test_one_head_then_more_of_one_buffer(layout):
     for G in (1, 8, 1, 2):
         q = buf[:, :G]
         check_attend(pages.attend(q, i32(lens)), q, codes, scales, table, lens, 0, 0.125)
+
+
+@pytest.mark.parametrize("hd,G", [(64, 2), (160, 4)])
+def test_attend_light_blocks_with_large_values(hd, G, layout):
+    """Blocks of weight e^-22 to e^-30 whose values are so much larger that
+    they make up a good part of the answer, next to ordinary ones in the same
+    warp: light and heavy in turn, light first or heavy first."""
+    rng = np.random.default_rng(29)
+    B, nb = 100, 32
+    codes, scales, table = pool(rng, B, nb // 2, 1, hd, fill=0x00)
+    a = [22.0, 24.0, 26.0, 28.0, 30.0]                     # E4M3 values
+    for b in range(B):
+        for j in range(nb):
+            pg, half = table[b, j // 2], j % 2
+            rows = slice(32 * half, 32 * half + 32)
+            k, v = codes[0][pg, 0, rows], codes[1][pg, 0, rows]
+            k[:, 1] = rng.integers(0x20, 0x38, 32)         # 1/8 .. 1
+            v[...] = rng.integers(0x30, 0x58, v.shape)     # 1/2 .. 16
+            v ^= rng.integers(0, 2, v.shape).astype(np.uint8) << 7
+            if (j + b) % 2:
+                x = a[(j + b) // 2 % 5]
+                k[:, 0] = oracle.encode(-x)
+                scales[1][pg, 0, half] = 2.0 ** round(x / np.log(2.0))
+    pages = pages_of(codes, scales, table)
+    q = np.zeros((B, G, hd))
+    q[..., 0] = 1.0
+    q[..., 1] = rng.uniform(0.1, 1.0, (B, G))
+    q = bf(q).cuda()
+    check_attend(pages.attend(q, i32([32 * nb] * B), scale=1.0), q, codes, scales, table,
+                 [32 * nb] * B, 0, 1.0)
+
+
+def test_small_weights_add_up_in_both_layouts(layout):
+    """8000 keys of weight e^-16 beside one of weight 1 (see
+    test_attend_small_weights_add_up), on pages of the layout's table."""
+    hd, n = 64, 8001
+    P = -(-n // 64)
+    codes, scales, table = pool(np.random.default_rng(30), 1, P, 1, hd, fill=0x00)
+    pages = pages_of(codes, scales, table)
+    k, v = np.zeros((2, 1, n, 1, hd))
+    k[0, 0, 0, 0] = 16.0
+    v[0, 1:] = 448.0
+    pages.append(bf(k).cuda(), bf(v).cuda(), i32([0]))
+    q = np.zeros((1, 1, hd))
+    q[..., 0] = 1.0
+    out = pages.attend(bf(q).cuda(), i32([n]), scale=1.0).double().cpu().numpy()
+    w = 8000 * np.exp(-16.0)
+    want = 448 * w / (1 + w)
+    assert np.all(np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -10) * want)
