@@ -187,8 +187,10 @@ class DoryModel:
         (temperature 0: greedy).  temperature, top_k, top_p and min_p are
         numbers or device tensors [B].  uniform: f32 [n_new, B] in [0, 1), or
         None to draw it from torch's generator.  Returns the new tokens int32
-        [B, n_new], and their log-probabilities f32 [B, n_new] if `logprobs`.
-        Runs on the current stream and waits for it once, at the end."""
+        [B, n_new], and their log-probabilities f32 [B, n_new] if `logprobs`;
+        a sequence with nothing to draw (dory_sample) is -1, and -inf, from
+        there on.  Runs on the device's current stream and waits for it once,
+        at the end."""
         home = self.device
         if (not isinstance(prompt, torch.Tensor) or prompt.dim() != 2
                 or prompt.dtype is not torch.int32 or not prompt.is_contiguous()
@@ -196,35 +198,39 @@ class DoryModel:
                 or home.index not in (None, prompt.device.index)
                 or 0 in prompt.shape):
             raise ValueError(f"prompt: contiguous int32 [B, T] on {home} is needed")
-        if n_new < 0 or (uniform is not None
-                         and uniform.shape != (n_new, prompt.shape[0])):
-            raise ValueError("n_new >= 0 and uniform [n_new, B] are needed")
         B, T = prompt.shape
         dev = prompt.device
+        if n_new < 0 or (uniform is not None and uniform.shape != (n_new, B)):
+            raise ValueError("n_new >= 0 and uniform [n_new, B] are needed")
 
         def option(x, dtype):
             if isinstance(x, torch.Tensor):
                 return x
             return torch.full((B,), x, dtype=dtype, device=dev)
 
-        opts = dict(temperature=option(temperature, torch.float32),
-                    top_k=option(top_k, torch.int32),
-                    top_p=option(top_p, torch.float32),
-                    min_p=option(min_p, torch.float32))
-        if uniform is None:
-            uniform = torch.rand((n_new, B), device=dev)
-        tokens = torch.empty((n_new, B), dtype=torch.int32, device=dev)
-        lps = torch.empty((n_new, B), dtype=torch.float32, device=dev)
-        cache = self.new_cache(B, T + n_new, T, kv_mode=kv_mode,
-                               max_loops=n_loops, kv_fmt=kv_fmt)
-        ws = self.workspace(B, T)
-        logits, _ = self.prefill(cache, prompt, n_loops, ws)
-        for i in range(n_new):
-            if i:
-                logits, _ = self.decode_step(cache, tokens[i - 1], n_loops, ws)
-            sample(logits, uniform[i], tokens=tokens[i], logprobs=lps[i], **opts)
-        tokens, lps = tokens.t().contiguous(), lps.t().contiguous()
-        torch.cuda.current_stream(dev).synchronize()   # before the cache goes
+        with torch.cuda.device(dev):
+            opts = dict(temperature=option(temperature, torch.float32),
+                        top_k=option(top_k, torch.int32),
+                        top_p=option(top_p, torch.float32),
+                        min_p=option(min_p, torch.float32))
+            if uniform is None:
+                uniform = torch.rand((n_new, B), device=dev)
+            tokens = torch.empty((n_new, B), dtype=torch.int32, device=dev)
+            lps = torch.empty((n_new, B), dtype=torch.float32, device=dev)
+            cache = self.new_cache(B, T + n_new, T, kv_mode=kv_mode,
+                                   max_loops=n_loops, kv_fmt=kv_fmt)
+            ws = self.workspace(B, T)
+            logits, _ = self.prefill(cache, prompt, n_loops, ws)
+            for i in range(n_new):
+                if i:
+                    # (a sequence that has stopped goes on with token 0)
+                    logits, _ = self.decode_step(cache, tokens[i - 1].clamp(min=0),
+                                                 n_loops, ws)
+                sample(logits, uniform[i], tokens=tokens[i], logprobs=lps[i], **opts)
+            ended = (tokens < 0).cumsum(0) > 0
+            tokens = tokens.masked_fill(ended, -1).t().contiguous()
+            lps = lps.masked_fill(ended, -float("inf")).t().contiguous()
+            torch.cuda.current_stream(dev).synchronize()   # before the cache goes
         return (tokens, lps) if logprobs else tokens
 
     def prefill_mixed(self, cache, tokens, row_loops, ws, logits_all=False,

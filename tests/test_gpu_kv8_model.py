@@ -329,3 +329,40 @@ def test_generate_refusals(tiny):
         with pytest.raises(ValueError):
             gm.generate(prompt, 3, 2, **kw)
     assert gm.generate(p, 0, 2).shape == (2, 0)
+
+
+def test_generate_where_nothing_can_be_drawn(tiny):
+    """All logits NaN: every token is -1, the log-probabilities are -inf, and
+    no device error is left for a later call to report."""
+    w, gm = tiny
+    bad = lb.DoryModel(TINY, dict(w, s_z=np.full_like(w["s_z"], np.nan)), device="cuda:0")
+    p = torch.from_numpy(make_prompt(TINY, 2, 12, seed=67)).cuda()
+    for opts in (dict(), dict(temperature=0.9, top_k=5)):
+        tok, lp = bad.generate(p, 4, 2, logprobs=True, **opts)
+        assert torch.all(tok == -1) and torch.all(lp == -np.inf)
+        assert bad.sync_status() == 0
+
+
+def test_generate_keeps_the_other_sequences_of_a_batch(tiny, monkeypatch):
+    """A sequence that stops is -1 from there on, whatever its later logits
+    are; the others go on as they would."""
+    _, gm = tiny
+    p = torch.from_numpy(make_prompt(TINY, 3, 12, seed=68)).cuda()
+    u = torch.rand(6, 3, device="cuda")
+    want, wlp = gm.generate(p, 6, 2, uniform=u, temperature=0.9, logprobs=True)
+    from looped_ngpt_b200 import model as module
+    real, calls = module.sample, []
+
+    def stops(logits, *args, **kw):
+        calls.append(None)
+        if len(calls) == 3:
+            logits = logits.clone()
+            logits[1] = -np.inf
+        return real(logits, *args, **kw)
+
+    monkeypatch.setattr(module, "sample", stops)
+    tok, lp = gm.generate(p, 6, 2, uniform=u, temperature=0.9, logprobs=True)
+    for b in (0, 2):
+        assert torch.equal(tok[b], want[b]) and torch.equal(lp[b], wlp[b])
+    assert torch.equal(tok[1, :2], want[1, :2])
+    assert torch.all(tok[1, 2:] == -1) and torch.all(lp[1, 2:] == -np.inf)
