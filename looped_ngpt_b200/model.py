@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from ._lib import DoryConfig, DoryTensor, check, KV_FMTS, KV_MODES
-from .ops import sample
+from .ops import _dense, sample
 
 
 def _stream_ptr(stream):
@@ -200,21 +200,26 @@ class DoryModel:
             raise ValueError(f"prompt: contiguous int32 [B, T] on {home} is needed")
         B, T = prompt.shape
         dev = prompt.device
-        if n_new < 0 or (uniform is not None and uniform.shape != (n_new, B)):
-            raise ValueError("n_new >= 0 and uniform [n_new, B] are needed")
+        if n_new < 0:
+            raise ValueError("n_new: 0 or more is needed")
+        if uniform is not None and not (
+                isinstance(uniform, torch.Tensor) and uniform.shape == (n_new, B)
+                and uniform.dtype is torch.float32 and uniform.device == dev):
+            raise ValueError(f"uniform: float32 [n_new, B] on {dev} is needed")
 
-        def option(x, dtype):
+        def option(x, name, dtype):
             if isinstance(x, torch.Tensor):
-                return x
+                return _dense(x, name, dtype, (B,), dev)
             return torch.full((B,), x, dtype=dtype, device=dev)
 
         with torch.cuda.device(dev):
-            opts = dict(temperature=option(temperature, torch.float32),
-                        top_k=option(top_k, torch.int32),
-                        top_p=option(top_p, torch.float32),
-                        min_p=option(min_p, torch.float32))
+            opts = dict(temperature=option(temperature, "temperature", torch.float32),
+                        top_k=option(top_k, "top_k", torch.int32),
+                        top_p=option(top_p, "top_p", torch.float32),
+                        min_p=option(min_p, "min_p", torch.float32))
             if uniform is None:
                 uniform = torch.rand((n_new, B), device=dev)
+            uniform = uniform.contiguous()
             tokens = torch.empty((n_new, B), dtype=torch.int32, device=dev)
             lps = torch.empty((n_new, B), dtype=torch.float32, device=dev)
             cache = self.new_cache(B, T + n_new, T, kv_mode=kv_mode,

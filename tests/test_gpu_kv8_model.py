@@ -366,3 +366,21 @@ def test_generate_keeps_the_other_sequences_of_a_batch(tiny, monkeypatch):
         assert torch.equal(tok[b], want[b]) and torch.equal(lp[b], wlp[b])
     assert torch.equal(tok[1, :2], want[1, :2])
     assert torch.all(tok[1, 2:] == -1) and torch.all(lp[1, 2:] == -np.inf)
+
+
+def test_generate_refuses_before_anything_is_enqueued(tiny, monkeypatch):
+    _, gm = tiny
+    p = torch.from_numpy(make_prompt(TINY, 2, 12, seed=69)).cuda()
+    u = torch.rand(3, 2, device="cuda")
+    monkeypatch.setattr(gm, "prefill", None)       # a call of it would raise TypeError
+    f = torch.ones(2, device="cuda")
+    for kw in (dict(uniform=u.double()), dict(uniform=u.cpu()), dict(uniform=u.cpu().numpy()),
+               dict(temperature=f.double()), dict(temperature=f[:1]), dict(top_k=f),
+               dict(top_p=f.cpu()), dict(min_p=f[None])):
+        with pytest.raises(ValueError):
+            gm.generate(p, 3, 2, **kw)
+    monkeypatch.undo()
+    # uniforms in any layout
+    a = gm.generate(p, 3, 2, uniform=u, temperature=1.0)
+    b = gm.generate(p, 3, 2, uniform=u.t().contiguous().t(), temperature=1.0)
+    assert torch.equal(a, b)
