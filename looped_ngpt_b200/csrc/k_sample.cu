@@ -1125,8 +1125,8 @@ __global__ void __launch_bounds__(kAnyThreads) sample_any_kernel(SampleArgs a) {
   const double inv_t = greedy ? 1.0 : 1.0 / (double)T;
   auto weight = [&](uint32_t k) -> double {
     if (k == mk) return 1.0;
-    const float v = key_float(k);
-    return v > -INFINITY ? exp(((double)v - (double)m) * inv_t) : 0.0;
+    const float v = key_float(k);            // (beside +inf nothing weighs anything)
+    return v > -INFINITY && m < INFINITY ? exp(((double)v - (double)m) * inv_t) : 0.0;
   };
   int n = a.top_k ? a.top_k[b] : 0;
   if (n <= 0 || n > V) n = V;

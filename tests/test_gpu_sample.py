@@ -229,3 +229,21 @@ def test_other_stream_and_graph_replay():
         g.replay()
         want, lp0 = lb.sample(z, u, top_p=p, logprobs=True)
         assert torch.equal(want, tok) and torch.equal(lp0, lp)
+
+
+@pytest.mark.parametrize("V", [262144, 262145])
+def test_infinite_temperature_and_logits_of_long_rows(V):
+    """Tokens at +inf share the row at any temperature, in rows of one cluster
+    and in longer ones."""
+    rng = np.random.default_rng(12)
+    z = logits(rng, 3, V)
+    z[0, [5, 70000, 200000]] = np.inf
+    z[1, [9, 250000]] = np.inf
+    z[1, 11] = -np.inf
+    z[2, ::2] = -np.inf
+    on_gpu = torch.tensor(z, device="cuda")
+    drawn = np.where((z == np.inf) | (z.max(1, keepdims=True) != np.inf), z, -np.inf)
+    for u in ([0.1, 0.1, 0.2], [0.5, 0.6, 0.9]):
+        for T in (1.0, np.inf):
+            run(drawn, u, T=[T] * 3, logits=on_gpu)
+            run(drawn, u, T=[T] * 3, p=[0.9] * 3, logits=on_gpu)
