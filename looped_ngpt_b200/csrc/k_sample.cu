@@ -1123,10 +1123,13 @@ __global__ void __launch_bounds__(kAnyThreads) sample_any_kernel(SampleArgs a) {
   const float T = a.temperature ? a.temperature[b] : 1.f;
   const bool greedy = !(T > 0.f);
   const double inv_t = greedy ? 1.0 : 1.0 / (double)T;
+  // Logits below `floor` weigh nothing, as in a cluster's rows; nor does -inf,
+  // or anything beside +inf
+  const float floor = m < INFINITY ? fmaxf(m - 44.f * T, -FLT_MAX) : m;
   auto weight = [&](uint32_t k) -> double {
     if (k == mk) return 1.0;
-    const float v = key_float(k);            // (beside +inf nothing weighs anything)
-    return v > -INFINITY && m < INFINITY ? exp(((double)v - (double)m) * inv_t) : 0.0;
+    const float v = key_float(k);
+    return v >= floor ? exp(((double)v - (double)m) * inv_t) : 0.0;
   };
   int n = a.top_k ? a.top_k[b] : 0;
   if (n <= 0 || n > V) n = V;

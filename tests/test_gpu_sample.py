@@ -247,3 +247,22 @@ def test_infinite_temperature_and_logits_of_long_rows(V):
         for T in (1.0, np.inf):
             run(drawn, u, T=[T] * 3, logits=on_gpu)
             run(drawn, u, T=[T] * 3, p=[0.9] * 3, logits=on_gpu)
+
+
+@pytest.mark.parametrize("V", [5000, 262145])
+def test_tokens_far_below_the_largest_are_not_drawn(V):
+    """Weights below e^-44 of the largest: not at the ends of the uniforms
+    either, where the oracle would draw them."""
+    z = np.zeros((4, V), np.float32)
+    z[:2, [0, V - 1]] = -60.0
+    z[:2, [1, V - 2]] = -30.0
+    z[2:, [0, V - 1]] = -20.0
+    z[2:, [1, V - 2]] = -10.0
+    T = [1.0, 1.0, 0.4, 0.4]                # -50 and -25
+    drawn = z.copy()
+    drawn[:, [0, V - 1]] = -np.inf
+    u = [0.0, 1.0, 0.0, 1.0]
+    on_gpu = torch.tensor(z, device="cuda")
+    for kw in ({}, dict(k=[V - 1] * 4), dict(mp=[1e-30] * 4)):
+        tok = run(drawn, u, T=T, logits=on_gpu, **kw)
+        assert kw.get("k") or list(tok) == [1, V - 2] * 2
