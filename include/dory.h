@@ -346,8 +346,8 @@ int dory_decode_step_mixed(dory_model* m, dory_cache* c,
  * -1 and log-probability -inf.  d_tokens int32 [B]; d_logprobs f32 [B] or NULL: the
  * log-probability of the token in the distribution it was drawn from.
  * Needs no workspace and allocates nothing.  Enqueued on `stream`.  Errors:
- * DORY_ERR_ARG (null pointer, B < 0, V < 1, ld < V), DORY_ERR_CUDA.
- * B = 0 is an empty call. */
+ * DORY_ERR_ARG (null pointer, B < 0, V < 1, ld < V), DORY_ERR_UNSUPPORTED
+ * (V > 2^30), DORY_ERR_CUDA.  B = 0 is an empty call. */
 int dory_sample(const float* d_logits, int64_t ld, int B, int V,
                 const float* d_temperature, const int32_t* d_top_k,
                 const float* d_top_p, const float* d_min_p,

@@ -1185,9 +1185,13 @@ __global__ void __launch_bounds__(kAnyThreads) sample_any_kernel(SampleArgs a) {
     }
     if (lo > cut) { cut = lo; ties = count_at(cut); }
     const double base = mass_above(cut), wc = weight(cut);
-    int r = 0;
-    while (r < ties && (base + r * wc < want || (cut == mk && r == 0))) ++r;
-    ties = r;
+    // the least r with base + r wc >= want (at least one token): a quotient,
+    // then to the side where the products say it is
+    int r = base < want ? ties : 0;
+    if (r && wc > 0.0) r = (int)fmin(ceil((want - base) / wc), (double)ties);
+    while (r > 0 && base + (r - 1) * wc >= want) --r;
+    while (r < ties && base + r * wc < want) ++r;
+    ties = min(ties, max(r, cut == mk ? 1 : 0));
   }
   const double kept = mass_above(cut) + ties * weight(cut);
   const float uf = a.uniform[b];

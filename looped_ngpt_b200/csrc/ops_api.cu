@@ -54,6 +54,7 @@ int dory_sample(const float* d_logits, int64_t ld, int B, int V,
                 const float* d_uniform, int32_t* d_tokens, float* d_logprobs,
                 void* stream) {
   if (B < 0 || V < 1 || ld < V) return DORY_ERR_ARG;
+  if (V > 1 << 30) return DORY_ERR_UNSUPPORTED;     // 32-bit loops over a row
   if (B == 0) return DORY_OK;
   if (!d_logits || !d_uniform || !d_tokens || !aligned(d_logits, 4)) return DORY_ERR_ARG;
   cudaGetLastError();

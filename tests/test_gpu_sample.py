@@ -266,3 +266,13 @@ def test_tokens_far_below_the_largest_are_not_drawn(V):
     for kw in ({}, dict(k=[V - 1] * 4), dict(mp=[1e-30] * 4)):
         tok = run(drawn, u, T=T, logits=on_gpu, **kw)
         assert kw.get("k") or list(tok) == [1, V - 2] * 2
+
+
+def test_long_rows_of_equal_logits():
+    """How many of a million equal tokens a top-p keeps is not counted one by
+    one."""
+    V = 1 << 20
+    z = np.zeros((4, V), np.float32)
+    z[2:, ::2] = 1.0
+    run(z, [0.2, 0.999, 0.4, 1.0], p=[0.5, 0.9, 0.6, 0.95])
+    run(z, [0.2, 0.999, 0.4, 1.0], p=[1e-9, 0.0, 1.0 - 2.0 ** -24, 0.3], k=[0, 0, 0, V // 2 + 5])

@@ -99,3 +99,11 @@ def test_python_refuses_what_is_not_on_a_gpu():
     s = torch.ones(2, 1, 2)
     with pytest.raises(ValueError, match="CUDA"):
         lb.KV8Pages(c, c, s, s, torch.zeros(1, 2, dtype=torch.int32))
+
+
+def test_sample_refuses_rows_past_its_loops():
+    """Rows near 2^31 would carry the kernel's 32-bit loops past their end."""
+    f = _lib.load().dory_sample
+    for V in (2 ** 30 + 1, 2 ** 31 - 1):
+        assert f(P, V, 1, V, None, None, None, None, P, P, None, None) == -2
+    assert f(P, 8, 0, 8, None, None, None, None, P, P, None, None) == 0
