@@ -716,9 +716,10 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
     };
     for (int level = 0;; ++level) {
       // histogram of the kept logits in [low, hi]
-      // bin of (hi - v) sc, rounded (monotone; the ends fall into the first and
-      // the last bin): in f32, or in f64 where the range of
-      // the logits or its reciprocal leaves f32's
+      // bin of (hi - v) sc, rounded to nearest (monotone; the ends fall into the
+      // first bin, half as wide as the others, and the last, half as wide again):
+      // in f32, or in f64 where the range of the logits or its reciprocal leaves
+      // f32's
       const float span = hi - low;
       const bool f32 = span > 1e-30f && span < 1e30f;
       const float sf = f32 ? (float)kNB / span : 0.f;
@@ -728,11 +729,11 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(SampleArgs a, i
         if (f32) {
 #pragma unroll
           for (int u = 0; u < N; ++u)
-            q[u] = __float_as_int(fmaf(hi - v[u], sf, 0x1.8p23f - 0.5f)) - 0x4b400000;
+            q[u] = __float_as_int(fmaf(hi - v[u], sf, 0x1.8p23f)) - 0x4b400000;
         } else {
 #pragma unroll
           for (int u = 0; u < N; ++u)
-            q[u] = __double2loint(fma(hd - (double)v[u], sc, 0x1.8p52 - 0.5));
+            q[u] = __double2loint(fma(hd - (double)v[u], sc, 0x1.8p52));
         }
 #pragma unroll
         for (int u = 0; u < N; ++u) q[u] = min(q[u], kNB - 1);
