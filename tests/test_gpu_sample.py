@@ -276,3 +276,32 @@ def test_long_rows_of_equal_logits():
     z[2:, ::2] = 1.0
     run(z, [0.2, 0.999, 0.4, 1.0], p=[0.5, 0.9, 0.6, 0.95])
     run(z, [0.2, 0.999, 0.4, 1.0], p=[1e-9, 0.0, 1.0 - 2.0 ** -24, 0.3], k=[0, 0, 0, V // 2 + 5])
+
+
+@pytest.mark.parametrize("T", [1.0, 0.7])
+def test_borders_are_off_by_less_than_2_to_the_minus_36(T):
+    """Two tokens of weights w and 1: token 0 is drawn for u < w / (1 + w).  Rows
+    are picked whose border lies between 2^-36 and 2^-34 of itself from the
+    nearest f32 uniform: a relative error of 2^-36 in w (2^-36 / (1 + w) in the
+    border) must not change the side; f64 sums and products add 2^-52."""
+    rng = np.random.default_rng(13)
+    z0 = -rng.uniform(0.01, 20.0, 1 << 22).astype(np.float32)
+    w = np.exp(z0.astype(np.longdouble) / np.longdouble(np.float32(T)))
+    border = w / (1 + w)
+    u = border.astype(np.float32)
+    rel = (border - u.astype(np.longdouble)) / border
+    pick = np.flatnonzero((np.abs(rel) >= 2.0 ** -36) & (np.abs(rel) <= 2.0 ** -34))
+    assert len(pick) > 1000
+    z = np.full((len(pick), 3), -np.inf, np.float32)
+    z[:, 0], z[:, 1] = z0[pick], 0.0
+    past = rel[pick] <= 0                          # u at the border or past it: token 1
+    dev = lambda a, dt: torch.tensor(a, dtype=dt, device="cuda")  # noqa: E731
+    n, zt, ut = len(pick), dev(z, torch.float32), dev(u[pick], torch.float32)
+    Tt = torch.full((n,), T, device="cuda")
+    for kw in ({}, dict(top_k=torch.full((n,), 2, dtype=torch.int32, device="cuda")),
+               dict(min_p=torch.full((n,), 1e-12, device="cuda"))):
+        # (min-p leaves out token 0 where it is lighter than that)
+        out = w[pick] < np.float32(1e-12) if "min_p" in kw else False
+        want = torch.tensor(past | out).int()
+        tok, _ = lb.sample(zt, ut, temperature=Tt, **kw)
+        assert torch.equal(tok.cpu(), want), (kw, int((tok.cpu() != want).sum()))
