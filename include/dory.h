@@ -406,17 +406,18 @@ int dory_kv8_append(const dory_kv8* c, const void* d_k, const void* d_v,
  * over positions j in [max(0, L - window), L), L = d_len[b] (window 0: from
  * 0), query head h reading KV head h / (n_q_heads / n_kv_heads).  d_q bf16
  * [batch][n_q_heads][head_dim] (q_strides: host array, element strides of
- * sequence and head, multiples of 8); d_out bf16, contiguous, and apart from
- * d_q.  L = 0 gives zeros.  Rows at positions >= L may hold anything.
- * n_q_heads / n_kv_heads must be 1, 2, 4 or 8.
+ * sequence and head, multiples of 8); d_out bf16, contiguous, apart from d_q
+ * (or d_q itself, where that is contiguous).  L = 0 gives zeros.  Rows at
+ * positions >= L may hold anything.  n_q_heads / n_kv_heads must be 1, 2, 4
+ * or 8.
  *   - Scores, softmax statistics and sums are f32.  Into the products go q as
  *     f16 after an exact shift of each row (elements below 2^-22 of the row's
- *     largest lose bits) and the weights as f16: rounded to 11 bits where
- *     they are above 2^-23 of the largest weight, and in 32-token blocks
- *     whose V scale is more than 4 times the smallest one, above 2^-23 of the
- *     block's largest; lighter ones are off by up to 2^-33 of the same.
- *     Weights below 2^-126 of the largest count as 0, and sums over keys
- *     overflow where |v| comes near f32's range.
+ *     largest lose bits) and the weights as f16: rounded to 11 bits above
+ *     2^-21 of the largest weight, off by up to 2^-32 of it below.  In
+ *     32-token blocks whose V scale is over 16 times the smallest one, of the
+ *     block's largest weight: light blocks of large values are safe.  Weights
+ *     below 2^-126 of the largest count as 0, and sums over keys overflow
+ *     where |v| comes near f32's range.
  *   - d_ws: dory_kv8_workspace_bytes, 256-byte aligned; its contents between
  *     calls are meaningless.  Calls that may run, or be enqueued by two
  *     threads, at the same time need workspaces of their own (a call is up to

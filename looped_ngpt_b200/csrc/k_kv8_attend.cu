@@ -34,11 +34,11 @@
 // rescaling and no reduction across lanes, just one vote).  K's scale joins the
 // score's factor.  V's scale, relative to the unit O is held in, joins the
 // exponent of p when within 2^2: an f16 weight below 2^-23 of the largest is
-// then off by up to 2^-34 of it.  The unit is the smallest scale so far, so
-// that such an error meets small values.  Blocks of larger scales have their
-// weights scaled by their own largest first and their product added in f32:
-// what is light may count as much as the rest by its values, down to weights of
-// 2^-126 of the largest (f32).
+// then off by up to 2^-34 of it, in O's unit.  The unit is the smallest scale
+// so far (up to 2^2), so that such an error meets small values.  Blocks of
+// larger scales have their weights scaled by their own largest first and their
+// product added in f32: what is light may count as much as the rest by its
+// values, down to weights of 2^-126 of the largest (f32).
 //
 // Row r = 8 i + perm(g) of a block (i < 4) is fragment row g.  Tiles carry the
 // swizzle of their row width (128, 64 or 32 bytes), and perm lets two

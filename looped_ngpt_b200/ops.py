@@ -50,6 +50,19 @@ def _rows(t, name, n):
     return s
 
 
+def _on_other_rows(out, q):
+    """Whether contiguous `out` [B, H, d] shares memory with q [B, H, d] (equal
+    sizes, last dim contiguous) and is not q itself."""
+    (B, H, d), (sb, sh, _) = q.shape, q.stride()
+    at, lo, hi = q.data_ptr(), out.data_ptr(), out.data_ptr() + 2 * out.numel()
+    if lo >= at + 2 * ((B - 1) * sb + (H - 1) * sh + d) or hi <= at:
+        return False
+    if at == lo and q.is_contiguous():
+        return False
+    rows = (at + 2 * (b * sb + h * sh) for b in range(B) for h in range(H))
+    return any(lo < r + 2 * d and r < hi for r in rows)
+
+
 def _cuda(t, name):
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise ValueError(f"{name}: a CUDA tensor is needed")
@@ -260,7 +273,8 @@ class KV8Pages:
         """Attention of one query per sequence, q bf16 [batch, n_q_heads,
         head_dim], over the lens[b] (int32 [batch]) cached tokens, the last
         `window` of them if window > 0; scale defaults to 1 / sqrt(head_dim).
-        Returns bf16 [batch, n_q_heads, head_dim] (`out`, if given).  Without
+        Returns bf16 [batch, n_q_heads, head_dim] (`out`, if given, which may
+        be a contiguous q itself).  Without
         `ws` this object keeps one workspace per stream (threads may share the
         stream), and a captured graph gets one of its own; a `ws` given is for
         one thread and one stream at a time."""
@@ -284,6 +298,8 @@ class KV8Pages:
             rows = self._q_rows = (key, _I64x2(*_rows(q, "q", 2)))
         if out is not None:
             _dense(out, "out", _BF16, shape, dev)
+            if _on_other_rows(out, q):
+                raise ValueError("out: overlaps other rows of q")
         if ws is not None and not (isinstance(ws, torch.Tensor) and ws.dtype is torch.uint8
                                    and ws.device == dev and ws.is_contiguous()):
             raise ValueError(f"ws: contiguous uint8 on {dev} is needed (workspace())")

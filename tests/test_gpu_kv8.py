@@ -630,3 +630,17 @@ def test_small_weights_add_up_in_both_layouts(layout):
     w = 8000 * np.exp(-16.0)
     want = 448 * w / (1 + w)
     assert np.all(np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -10) * want)
+
+
+@pytest.mark.parametrize("hd,H,G", [(64, 2, 4), (160, 4, 4)])
+def test_output_in_place_of_the_query(hd, H, G, layout):
+    """`out` = q gives the bits of an output of its own."""
+    rng = np.random.default_rng(31)
+    lens = [0, 1, 200, 700, 33, 64, 1000, 1000]
+    pages, codes, scales, table = filled(rng, lens, 16, H, hd)
+    q = bf(rng.standard_normal((len(lens), H * G, hd))).cuda()
+    for window in (0, 100):
+        want = pages.attend(q, i32(lens), window=window)
+        mine = q.clone()
+        got = pages.attend(mine, i32(lens), window=window, out=mine)
+        assert got.data_ptr() == mine.data_ptr() and torch.equal(mine, want)

@@ -128,3 +128,22 @@ def test_workspaces_that_do_not_fit(lib):
     assert not lib.launches
     p.attend(q, lens, ws=ws)
     assert lib.launches[0][0] == ws.data_ptr()
+
+
+def test_outputs_that_overlap_the_query(lib):
+    """`out` may be the query itself (a pair's query has been read when its
+    output is written) or lie between its rows, but not on other rows of it."""
+    p, lens = pages(heads=2), torch.zeros(3, dtype=torch.int32)
+    buf = torch.zeros(2 * 3 * 256, dtype=BF16)
+    q = buf[:3 * 256].view(3, 4, 64)
+    for at in (8, 64, 256, 512):
+        with pytest.raises(ValueError, match="overlap"):
+            p.attend(q, lens, out=buf[at:at + 3 * 256].view(3, 4, 64))
+    big = torch.zeros(3, 5, 4, 64, dtype=BF16)
+    with pytest.raises(ValueError, match="overlap"):
+        p.attend(big[:, 1], lens, out=big[0, 1:4])
+    assert not lib.launches
+    p.attend(q, lens, out=q)
+    p.attend(big[:, 1], lens, out=big[0, 2:5])          # before the second row
+    p.attend(q, lens, out=torch.zeros_like(q))
+    assert len(lib.launches) == 6
