@@ -156,6 +156,16 @@ def sample(logits, uniform, temperature=None, top_k=None, top_p=None,
         return enqueue(st, tokens, lp)
 
 
+class _Workspaces(threading.local):
+    """A thread's workspaces by (stream, heads).  An attention is two launches,
+    the second of which reads what the first left in the workspace, and the
+    interpreter lock is let go meanwhile: another thread on the same stream
+    needs a workspace of its own."""
+
+    def __init__(self):
+        self.kept = {}
+
+
 class KV8Pages:
     """One attention layer's K/V entries in 8 bits (dory_kv8): E4M3 codes in
     64-token pages behind a block table, one power-of-two scale per 32 tokens
@@ -189,6 +199,7 @@ class KV8Pages:
         self.block_table, self.device = block_table, dev
         self.n_kv_heads, self.head_dim = shape[1], shape[3]
         self.batch, self.pages_per_seq = block_table.shape
+        self._room = self.pages_per_seq * PAGE           # tokens of a sequence
         self.c = DoryKv8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
                          v_scale.data_ptr(), block_table.data_ptr(), shape[0],
                          self.pages_per_seq, self.batch, shape[1], shape[3])
@@ -198,10 +209,7 @@ class KV8Pages:
         plan = -(-ctypes.addressof(self._plan) // 64) * 64
         check("dory_kv8_plan", _lib.load().dory_kv8_plan(self._ref, plan))
         self.c.plan = plan
-        # workspaces by (stream, heads).  A call is two launches, the second of
-        # which reads what the first left in the workspace, and the interpreter
-        # lock is let go meanwhile: held over both
-        self._ws, self._ws_lock = {}, threading.Lock()
+        self._ws = _Workspaces()
         self._rows = self._q_rows = (None,)
         self._q_heads = [g * shape[1] for g in (1, 2, 4, 8)]
 
@@ -275,9 +283,9 @@ class KV8Pages:
         `window` of them if window > 0; scale defaults to 1 / sqrt(head_dim).
         Returns bf16 [batch, n_q_heads, head_dim] (`out`, if given, which may
         be a contiguous q itself).  Without
-        `ws` this object keeps one workspace per stream (threads may share the
-        stream), and a captured graph gets one of its own; a `ws` given is for
-        one thread and one stream at a time."""
+        `ws` this object keeps one workspace per stream and thread, and a
+        captured graph gets one of its own; a `ws` given is for one thread and
+        one stream at a time."""
         dev, B, hd = self.device, self.batch, self.head_dim
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q: bf16 [batch, n_q_heads, head_dim] is needed")
@@ -291,7 +299,8 @@ class KV8Pages:
         _dense(lens, "lens", _I32, (B,), dev)
         if window < 0:
             raise ValueError("window: 0 (off) or more is needed")
-        window = min(window, self.pages_per_seq * PAGE)
+        if window > self._room:
+            window = self._room
         key, pq = (Hq, q.stride()), q.data_ptr()
         rows = self._q_rows
         if key != rows[0] or pq % 16:
@@ -318,19 +327,13 @@ class KV8Pages:
                    else torch.empty(q.shape, dtype=_BF16, device=self.device))
         if ws is None and torch.cuda.is_current_stream_capturing():
             ws = self.workspace(Hq)          # the graph's own
-        if ws is not None:
-            self._enqueue(st, pq, strides, Hq, lens, window, scale, out, ws)
-            return out
-        with self._ws_lock:
-            ws = self._ws.get((st, Hq))
+        elif ws is None:
+            ws = self._ws.kept.get((st, Hq))
             if ws is None:
-                ws = self._ws[st, Hq] = self.workspace(Hq)
-            self._enqueue(st, pq, strides, Hq, lens, window, scale, out, ws)
-        return out
-
-    def _enqueue(self, st, pq, strides, Hq, lens, window, scale, out, ws):
+                ws = self._ws.kept[st, Hq] = self.workspace(Hq)
         rc = _lib.load().dory_kv8_attend(
             self._ref, pq, strides, Hq, lens.data_ptr(), window, scale,
             out.data_ptr(), ws.data_ptr(), ws.numel(), st)
         if rc:
             check("dory_kv8_attend", rc)
+        return out

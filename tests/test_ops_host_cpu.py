@@ -52,8 +52,8 @@ def pages(heads=1, batch=3):
 
 
 def test_threads_on_one_stream_do_not_mix_their_launches(lib):
-    """The kept workspace carries pieces from the attention to the kernel that
-    joins them: no other call on the stream may come between the two."""
+    """A workspace carries pieces from the attention to the kernel that joins
+    them: no other call may use it between the two."""
     p, lens = pages(), torch.zeros(3, dtype=torch.int32)
 
     def work():
@@ -67,9 +67,10 @@ def test_threads_on_one_stream_do_not_mix_their_launches(lib):
     for t in threads:
         t.join()
     assert len(lib.launches) == 30
-    assert len({ws for ws, _, _ in lib.launches}) == 1
-    for a, m in zip(lib.launches[::2], lib.launches[1::2]):
-        assert (a[1], m[1]) == ("attend", "merge") and a[2] == m[2]
+    for ws in {ws for ws, _, _ in lib.launches}:
+        mine = [x for x in lib.launches if x[0] == ws]
+        for a, m in zip(mine[::2], mine[1::2]):
+            assert (a[1], m[1]) == ("attend", "merge") and a[2] == m[2]
 
 
 def test_strides_of_one_head_are_not_kept_for_more(lib):
