@@ -339,12 +339,13 @@ int dory_decode_step_mixed(dory_model* m, dory_cache* c,
  * kept sum (u outside [0, 1) is clamped; the last kept token for u = 1).
  * Sums are f64, weights f64 with a relative error below 2^-36, and top-p
  * compares and sums them as integers of 43 bits (V up to 262144; above, one
- * block per row works in f64 throughout, and is slow): a uniform, or a share,
- * that lies closer to a border than that may fall to its other side.  Tokens
- * below e^-44 of the largest weight are not drawn, nor is a -inf or NaN logit;
- * tokens at +inf share the row equally; a row with nothing to draw gets token
- * -1 and log-probability -inf.  d_tokens int32 [B]; d_logprobs f32 [B] or NULL: the
- * log-probability of the token in the distribution it was drawn from.
+ * block per row works in f64 throughout: 0.6 to 4 ms for V = 262208): a
+ * uniform, or a share, that lies closer to a border than that may fall to its
+ * other side.  Tokens below e^-44 of the largest weight are not drawn, nor is
+ * a -inf or NaN logit; tokens at +inf share the row equally; a row with nothing
+ * to draw gets token -1 and log-probability -inf.  d_tokens int32 [B];
+ * d_logprobs f32 [B] or NULL: the log-probability of the token in the
+ * distribution it was drawn from.
  * Needs no workspace and allocates nothing.  Enqueued on `stream`.  Errors:
  * DORY_ERR_ARG (null pointer, B < 0, V < 1, ld < V), DORY_ERR_UNSUPPORTED
  * (V > 2^30), DORY_ERR_CUDA.  B = 0 is an empty call. */

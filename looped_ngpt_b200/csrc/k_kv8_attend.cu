@@ -20,8 +20,8 @@
 // Where there are few pairs of short sequences each pair gets a cluster of up
 // to 16 thread blocks instead, which share its blocks in the same way and join
 // their pieces in each other's shared memory: one launch, no prefix sum over
-// the lengths (head_dim 160, 4 KV heads, against runs: 1 sequence of 2048 7.1
-// for 9.2 us, 16 of 1024 9.5 for 12.0 us).
+// the lengths (head_dim 160, 4 KV heads, against runs: 1 sequence of 2048 7.2
+// for 9.3 us, 16 of 1024 9.6 for 12.0 us).
 //
 // One block in a warp: S^T = K Q^T on m16n8k16 (keys as A rows, the heads as
 // the 8 columns), online softmax per head (lane 4g + t owns heads 2t, 2t+1),
@@ -47,11 +47,13 @@
 // TMA instruction per tile: the same blocks as 16 bulk copies of 4 rows cost
 // 160 issue slots per block, a third of the kernel's instructions.)
 //
-// Times (head_dim 160, 4 query heads per KV head, 4 KV heads, of 6.55 TB/s):
-// 64 sequences of 32768 tokens 414 us (99%), 4 of 131072 114 us (90%), one of
-// 2048 7 us, a chain of length -> page -> tile -> product -> join.  48 sequences
-// of up to 9001 tokens behind a 1024-token window (head_dim 128, 8 x 8 heads)
-// take 32 us (46%): 10 blocks per warp do not amortise that chain.
+// Times in a graph of calls (head_dim 160, 4 query heads per KV head, 4 KV
+// heads, of 6.55 TB/s): 64 sequences of 32768 tokens 416 us (98%), 4 of 131072
+// 114 us (90%), one of 2048 7.2 us, a chain of length -> page -> tile -> product
+// -> join (9.3 us where the block table is much longer than the sequence, as the
+// form is chosen by the table).  48 sequences of up to 9001 tokens behind a
+// 1024-token window (head_dim 128, 8 x 8 heads) take 32 us (46%): 10 blocks per
+// warp do not amortise that chain.
 #include <algorithm>
 
 #include "async_copy.cuh"
