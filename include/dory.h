@@ -413,12 +413,11 @@ int dory_kv8_append(const dory_kv8* c, const void* d_k, const void* d_v,
  * or 8.
  *   - Scores, softmax statistics and sums are f32.  Into the products go q as
  *     f16 after an exact shift of each row (elements below 2^-22 of the row's
- *     largest lose bits) and the weights as f16: rounded to 11 bits above
- *     2^-21 of the largest weight, off by up to 2^-32 of it below.  In
- *     32-token blocks whose V scale is over 16 times the smallest one, of the
- *     block's largest weight: light blocks of large values are safe.  Weights
- *     below 2^-126 of the largest count as 0, and sums over keys overflow
- *     where |v| comes near f32's range.
+ *     largest lose bits) and the weights as f16: rounded to 11 bits, or off by
+ *     up to 2^-32 of the largest weight among the 32-token blocks whose V scale
+ *     is at least 1/16 of their own's (so light blocks of large values keep
+ *     their bits).  Weights below 2^-126 of the largest count as 0, and sums
+ *     over keys overflow where |v| comes near f32's range.
  *   - d_ws: dory_kv8_workspace_bytes, 256-byte aligned; its contents between
  *     calls are meaningless.  Calls that may run, or be enqueued by two
  *     threads, at the same time need workspaces of their own (a call is up to

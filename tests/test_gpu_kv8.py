@@ -644,3 +644,44 @@ def test_output_in_place_of_the_query(hd, H, G, layout):
         mine = q.clone()
         got = pages.attend(mine, i32(lens), window=window, out=mine)
         assert got.data_ptr() == mine.data_ptr() and torch.equal(mine, want)
+
+
+@pytest.mark.parametrize("spread", [1, 20, 60])
+@pytest.mark.parametrize("hd,B,n", [(64, 150, 300), (128, 7, 1000), (160, 40, 96)])
+def test_attend_holds_its_stated_bound(hd, B, n, spread, layout):
+    """Keys of random codes and steep scores: the heaviest key's values may be
+    2^-9 in units where a light one's are 448.  Beside the output's rounding
+    (2^-8 |o|) and 11-bit weights (2^-10 A, see the module) a weight may be off
+    by 2^-32 of the largest among the blocks whose V scale is at least 1/16 of
+    its own block's.  An f32 score is a sum of hd products and errs by at most
+    hd 2^-23 sum |q k| scale, which is the relative error of its weight."""
+    rng = np.random.default_rng(hd + spread)
+    H, G, P, scale = 1, 2, -(-n // 64), 1.0
+    codes, scales, table = pool(rng, B, P, H, hd, fill=0x00)
+    for c in codes:
+        c[...] = rng.integers(0, 0x7F, c.shape)
+        c[...] ^= rng.integers(0, 2, c.shape).astype(np.uint8) << 7
+    scales[0][...] = 2.0 ** rng.integers(-12, -6, scales[0].shape)
+    scales[1][...] = 2.0 ** rng.integers(-spread, spread + 1, scales[1].shape)
+    lens = [n] + [int(x) for x in rng.integers(1, n + 1, B - 1)]
+    pages = pages_of(codes, scales, table)
+    q = bf(rng.standard_normal((B, H * G, hd))).cuda()
+    out = pages.attend(q, i32(lens), scale=scale).double().cpu().numpy()
+    qd = q.double().cpu().numpy()
+    for b in range(B):
+        (ck, sk), (cv, sv) = [seq_view(c, s, table, b, 0) for c, s in zip(codes, scales)]
+        k, v = oracle.decode(ck, sk, lens[b]), oracle.decode(cv, sv, lens[b])
+        o, A = oracle.attend(qd[b], k, v, 0, scale)
+        z = scale * (qd[b] @ k.T)
+        w = np.exp(z - z.max(1, keepdims=True))
+        w /= w.sum(1, keepdims=True)
+        nb = -(-lens[b] // 32)
+        first = np.arange(nb) * 32
+        heaviest = np.maximum.reduceat(w, first, axis=1)             # [G, nb]
+        allowed = sv[None, :nb] >= sv[:nb, None] / 16                # [nb, nb]
+        ref = np.where(allowed[None], heaviest[:, None, :], 0.0).max(-1)
+        lost = 2.0 ** -32 * (ref @ np.add.reduceat(np.abs(v), first, axis=0))
+        e = hd * 2.0 ** -23 * scale * (np.abs(qd[b]) @ np.abs(k).T).max(1, keepdims=True)
+        bound = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + e) * A + lost
+        err = np.abs(out[b] - o)
+        assert np.all(err <= bound), (b, lens[b], float((err / bound).max()))
