@@ -55,6 +55,7 @@
 // 1024-token window (head_dim 128, 8 x 8 heads) take 32 us (46%): 10 blocks per
 // warp do not amortise that chain.
 #include <algorithm>
+#include <mutex>
 
 #include "async_copy.cuh"
 #include "common.cuh"
@@ -818,8 +819,7 @@ int attend_grid() {
   return n[dev];
 }
 
-// What a device takes of one instantiation: set up once (twice, if two threads
-// meet here).
+// What a device takes of one instantiation, set up once.
 struct Fit {
   bool set;
   int clusters[5];                     // at a time, of 1, 2, 4, 8 and 16 thread blocks
@@ -828,8 +828,10 @@ struct Fit {
 template <int HD, int G>
 Fit fit_of() {
   using L = Att<HD>;
+  static std::mutex mu;
   static Fit fit[kMaxDevices];
   int dev = 0;
+  std::lock_guard<std::mutex> lock(mu);
   const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices;
   if (known && fit[dev].set) return fit[dev];
   Fit f = {};
